@@ -10,6 +10,7 @@ Two layers, same names as the C ABI:
   * ``quantize_1x128(x, ...)``, ``quantize_128x128``, ``quantize_mx32``, ``quantize_tensor``,
     ``rht16_quantize_sr``, ``gemm`` take torch tensors, allocate the outputs and call them.
 """
+import contextlib
 import ctypes
 import os
 
@@ -26,7 +27,10 @@ __all__ = [
     "quantize_1x128", "quantize_128x128", "quantize_128x128_grouped", "quantize_tensor_delayed", "quantize_mx32", "quantize_tensor", "rht16_quantize_sr",
     "quantize_nvfp4_2d16", "gemm", "gemm_workspace_bytes", "device_status", "EXPORTED_SYMBOLS",
     "fp8q_quantize_multi", "fp8q_gemm_workspace_bytes", "QuantItem", "FP8Q_ITEM_1X128", "FP8Q_ITEM_128X128", "FP8Q_MAX_QUANT_ITEMS",
-    "quantize_multi",
+    "quantize_multi", "fp8q_grouped_capacity", "fp8q_quantize_1x128_grouped", "quantize_1x128_grouped",
+    "fp8q_clip_grad_norm", "fp8q_clip_grad_workspace_bytes", "GradItem", "clip_grad_norm", "FP8Q_BF16", "FP8Q_FP32",
+    "fp8q_norm_residual", "fp8q_norm_residual_backward", "fp8q_norm_backward_workspace_bytes", "NormArgs",
+    "NormBackwardArgs", "norm_residual", "norm_residual_backward",
 ]
 
 FP8Q_OK = 0
@@ -38,6 +42,7 @@ FP8Q_SF_ROWMAJOR, FP8Q_SF_MMA_TILED = 0, 1
 FP4Q_ROW, FP4Q_COL = 1, 2
 FP8Q_E4M3, FP8Q_E5M2 = 0, 1
 FP8Q_ITEM_1X128, FP8Q_ITEM_128X128 = 0, 1
+FP8Q_BF16, FP8Q_FP32 = 0, 1
 FP8Q_MAX_QUANT_ITEMS = 8
 
 EXPORTED_SYMBOLS = [
@@ -46,6 +51,9 @@ EXPORTED_SYMBOLS = [
     "fp8q_release_scratch", "fp8q_status_string", "fp8q_version", "fp8q_quantize_tensor_noalloc",
     "fp8q_selftest_bounded_wait", "fp8q_quantize_128x128_grouped", "fp8q_quantize_tensor_delayed",
     "fp4q_quantize_2d16", "fp8q_quantize_multi", "fp8q_gemm_workspace_bytes",
+    "fp8q_grouped_capacity", "fp8q_quantize_1x128_grouped",
+    "fp8q_clip_grad_norm", "fp8q_clip_grad_workspace_bytes", "fp8q_norm_residual", "fp8q_norm_residual_backward",
+    "fp8q_norm_backward_workspace_bytes",
 ]
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8q.so")
@@ -65,6 +73,40 @@ class QuantItem(ctypes.Structure):
         ("q_row", ctypes.c_void_p), ("s_row", ctypes.c_void_p), ("ld_s_row", ctypes.c_int64),
         ("q_col", ctypes.c_void_p), ("s_col", ctypes.c_void_p), ("ld_s_col", ctypes.c_int64),
         ("q_t", ctypes.c_void_p), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p),
+    ]
+
+
+class GradItem(ctypes.Structure):
+    """Mirror of fp8q_grad_item (field order and types as in include/fp8q.h)."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int64)]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of fp8q_norm_args (field order and types as in include/fp8q.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("h_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+        ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+        ("h_out", ctypes.c_void_p), ("ld_h_out", ctypes.c_int64), ("n_out", ctypes.c_void_p), ("ld_n", ctypes.c_int64),
+        ("q_row", ctypes.c_void_p), ("s_row", ctypes.c_void_p), ("ld_s_row", ctypes.c_int64),
+        ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p),
+    ]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    """Mirror of fp8q_norm_backward_args (field order and types as in include/fp8q.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("h_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+        ("alpha", ctypes.c_float),
+        ("dn", ctypes.c_void_p), ("ld_dn", ctypes.c_int64), ("dh_out", ctypes.c_void_p), ("ld_dh_out", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+        ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+        ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p),
+        ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64), ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+        ("dw_post", ctypes.c_void_p), ("dgate", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -101,6 +143,10 @@ def lib():
         L.fp8q_quantize_1x128.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
         L.fp8q_quantize_128x128.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]
         L.fp8q_quantize_128x128_grouped.argtypes = [_vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp]
+        L.fp8q_grouped_capacity.argtypes = [_i64, ctypes.c_int32]
+        L.fp8q_grouped_capacity.restype = _i64
+        L.fp8q_quantize_1x128_grouped.argtypes = [_vp, _i64, _i64, _i64, _vp, ctypes.c_int32, _vp, _vp, _i64,
+                                                  _vp, _vp, _i64, _vp]
         L.fp8q_quantize_mx32.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _int, _vp]
         L.fp8q_quantize_tensor.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
         L.fp8q_quantize_tensor_noalloc.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
@@ -113,6 +159,13 @@ def lib():
         L.fp8q_gemm_workspace_bytes.argtypes = [ctypes.POINTER(GemmArgs)]
         L.fp8q_gemm_workspace_bytes.restype = ctypes.c_size_t
         L.fp8q_quantize_multi.argtypes = [ctypes.POINTER(QuantItem), ctypes.c_int32, _vp]
+        L.fp8q_norm_residual.argtypes = [ctypes.POINTER(NormArgs), _vp]
+        L.fp8q_norm_residual_backward.argtypes = [ctypes.POINTER(NormBackwardArgs), _vp]
+        L.fp8q_norm_backward_workspace_bytes.argtypes = [_i64, _i64, ctypes.c_int32]
+        L.fp8q_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.fp8q_clip_grad_norm.argtypes = [_vp, _i64, ctypes.c_double, ctypes.c_double, _vp, _vp, _i64, _vp]
+        L.fp8q_clip_grad_workspace_bytes.argtypes = [_i64]
+        L.fp8q_clip_grad_workspace_bytes.restype = ctypes.c_size_t
         L.fp8q_sf_bytes.argtypes = [_int, _i64, _i64, _int]
         L.fp8q_sf_bytes.restype = ctypes.c_size_t
         L.fp8q_get_device_status.argtypes = [_vp]
@@ -130,7 +183,9 @@ def lib():
                                                      "fp8q_get_device_status", "fp8q_release_scratch",
                                                      "fp8q_selftest_bounded_wait", "fp8q_quantize_128x128_grouped",
                                                      "fp8q_quantize_tensor_delayed", "fp4q_quantize_2d16",
-                                                     "fp8q_quantize_multi"):
+                                                     "fp8q_quantize_multi", "fp8q_quantize_1x128_grouped",
+                                                     "fp8q_clip_grad_norm", "fp8q_norm_residual",
+                                                     "fp8q_norm_residual_backward"):
                 f.restype = ctypes.c_int
         _LIB = L
     return _LIB
@@ -154,6 +209,13 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(device, stream):
+    """Makes `device` current for a call on its tensors (and refuses a stream of another device)."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -174,6 +236,16 @@ def fp8q_quantize_multi(items, n_items, stream):
 
 def fp8q_quantize_128x128_grouped(w, groups, K, N, ld_w, q_t, q, s, stream):
     return lib().fp8q_quantize_128x128_grouped(w, groups, K, N, ld_w, q_t, q, s, stream)
+
+
+def fp8q_grouped_capacity(rows, groups):
+    return int(lib().fp8q_grouped_capacity(rows, groups))
+
+
+def fp8q_quantize_1x128_grouped(x, rows, cols, ld_x, offsets, groups, q_row, s_row, ld_s_row, q_col, s_col, ld_s_col,
+                                stream):
+    return lib().fp8q_quantize_1x128_grouped(x, rows, cols, ld_x, offsets, groups, q_row, s_row, ld_s_row, q_col,
+                                             s_col, ld_s_col, stream)
 
 
 def fp8q_quantize_mx32(x, rows, cols, ld_x, q_row, e_row, q_col, e_col, sf_layout, stream):
@@ -210,6 +282,27 @@ def fp8q_gemm_blockscaled(args, stream):
 
 def fp8q_gemm_workspace_bytes(args):
     return lib().fp8q_gemm_workspace_bytes(ctypes.byref(args))
+
+
+def fp8q_norm_residual(args, stream):
+    return lib().fp8q_norm_residual(ctypes.byref(args), stream)
+
+
+def fp8q_norm_residual_backward(args, stream):
+    return lib().fp8q_norm_residual_backward(ctypes.byref(args), stream)
+
+
+def fp8q_norm_backward_workspace_bytes(rows, cols, h_dtype):
+    return int(lib().fp8q_norm_backward_workspace_bytes(rows, cols, h_dtype))
+
+
+def fp8q_clip_grad_norm(items, n_items, max_norm, eps, norm, workspace, workspace_bytes, stream):
+    """items: a ctypes array of GradItem (or None with n_items == 0)."""
+    return lib().fp8q_clip_grad_norm(items, n_items, max_norm, eps, norm, workspace, workspace_bytes, stream)
+
+
+def fp8q_clip_grad_workspace_bytes(n_items):
+    return int(lib().fp8q_clip_grad_workspace_bytes(n_items))
 
 
 def fp8q_sf_bytes(recipe, outer, inner, layout):
@@ -338,6 +431,39 @@ def quantize_128x128_grouped(w, transposed=True, plain=True, stream=None):
     return out
 
 
+def _check_offsets(m_offsets, device):
+    if not (m_offsets.device == device and m_offsets.dtype == torch.int32 and m_offsets.dim() == 1
+            and m_offsets.is_contiguous() and m_offsets.numel() >= 2):
+        raise ValueError("m_offsets must be a contiguous 1-D int32 tensor of groups + 1 offsets on the operands' device")
+
+
+def quantize_1x128_grouped(x, m_offsets, rowwise=False, colwise=True, stream=None):
+    """1x128 tiles of routed tokens x (R, C), expert g's being rows m_offsets[g] .. m_offsets[g + 1] - 1 (int32
+    CUDA tensor of groups + 1), with no tile over two experts' tokens.  Returns q_col (C, P) uint8, s_col
+    (P/128, C) float32 on the padded token axis P = fp8q_grouped_capacity(R, groups), the grouped WGRAD operands
+    of gemm(), and with rowwise q_row (R, C), s_row (C/128, R) as quantize_1x128 returns them."""
+    _check_bf16(x)
+    _check_offsets(m_offsets, x.device)
+    if not colwise:
+        raise ValueError("grouping only concerns the colwise output: use quantize_1x128 for rowwise alone")
+    R, C = x.shape
+    groups = m_offsets.numel() - 1
+    P = fp8q_grouped_capacity(R, groups)
+    dev = x.device
+    out = {"q_col": torch.empty((C, P), dtype=torch.uint8, device=dev),
+           "s_col": torch.empty((P // 128, C + (-C) % 4), dtype=torch.float32, device=dev)}
+    if rowwise:
+        out["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        out["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
+    with _on(dev, stream):
+        st = fp8q_quantize_1x128_grouped(_ptr(x), R, C, x.stride(0), _ptr(m_offsets), groups, _ptr(out.get("q_row")),
+                                         _ptr(out.get("s_row")), out["s_row"].shape[1] if rowwise else 0,
+                                         _ptr(out["q_col"]), _ptr(out["s_col"]), out["s_col"].shape[1],
+                                         _stream(stream))
+    _check(st, "fp8q_quantize_1x128_grouped")
+    return out
+
+
 def quantize_mx32(x, rowwise=True, colwise=False, sf_layout=FP8Q_SF_ROWMAJOR, stream=None):
     """MXFP8.  Returns q_row (R, C) + e8m0_row, and/or q_col (C, R) + e8m0_col (flat uint8
     buffers sized by fp8q_sf_bytes for the chosen layout)."""
@@ -432,12 +558,25 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
     """The C ABI's argument block for gemm() (and the output tensor it writes)."""
     M = a.shape[0]
     grouped = m_offsets is not None
-    N = b.shape[1] if grouped else b.shape[0]
+    if grouped:
+        _check_offsets(m_offsets, a.device)
+    k_groups = grouped and layout == FP8Q_WGRAD        # experts split K; C is stacked
+    groups = m_offsets.numel() - 1 if grouped else 0
+    if grouped and any(t is not None and t.device != m_offsets.device for t in (b, a_scale, b_scale, out)):
+        raise ValueError("grouped operands must be on one device")
+    if grouped and b.dim() != (2 if k_groups else 3):
+        raise ValueError("grouped b must be (G, N, K) codes, or (N, P) on the padded token axis for WGRAD")
+    if grouped and not k_groups and (b.shape[0] != groups or b.stride(0) != b.shape[1] * b.stride(1)):
+        raise ValueError("b must hold one matrix per expert, one directly after the other")
+    N = b.shape[-2]
     if K is None:
         K = a.shape[1] * (2 if recipe == FP8Q_NVFP4 else 1)
     if accumulate_fp32 and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate_fp32 needs an FP32 `out` tensor to update")
-    c = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    shape = (groups, M, N) if k_groups else (M, N)
+    c = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=a.device)
+    if k_groups and (tuple(c.shape) != shape or c.stride(2) != 1 or c.stride(0) != M * c.stride(1)):
+        raise ValueError("grouped WGRAD `out` must be (G, M, N), one matrix directly after the other")
     args = GemmArgs()
     args.recipe, args.layout = recipe, layout
     args.M, args.N, args.K = M, N, K
@@ -449,9 +588,9 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
     args.ld_sb = ld_sb if ld_sb is not None else (b_scale.shape[-1] if (b_scale is not None and b_scale.dim() >= 2) else 0)
     args.a_global = a_global.data_ptr() if a_global is not None else None
     args.b_global = b_global.data_ptr() if b_global is not None else None
-    args.c, args.ldc = c.data_ptr(), c.stride(0)
+    args.c, args.ldc = c.data_ptr(), c.stride(-2)
     args.m_offsets = m_offsets.data_ptr() if grouped else None
-    args.num_groups = (m_offsets.numel() - 1) if grouped else 0
+    args.num_groups = groups
     args.c_fp32_accumulate = 1 if accumulate_fp32 else 0
     args.a_format, args.b_format = a_format, b_format
     if q_out is not None or s_out is not None:
@@ -467,6 +606,10 @@ def gemm(a, b, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, a_scale=None, b_scale=N
          a_format=0, b_format=0, q_out=None, s_out=None, stream=None, split_tail=True):
     """C = A . B^T (BF16).  a: (M, K or K/2) uint8 codes, b: (N, ...) or (G, N, ...) uint8.
     Scales as the C ABI describes for the recipe.  Returns C (M, N) bf16.
+    m_offsets (BLOCKWISE; int32 CUDA tensor of G + 1): products grouped by expert.  FPROP and DGRAD: expert g's
+    rows of a and C are m_offsets[g] .. m_offsets[g + 1] - 1, b is (G, N, K) and b_scale stacked likewise.
+    WGRAD: a (M, P) and b (N, P) are quantize_1x128_grouped's colwise codes for the same offsets, and C is
+    (G, M, N), expert g's product running over its own tokens only.
     accumulate_fp32 (BLOCKWISE): `out` is an FP32 (M, N) tensor updated in place, C += A . B^T.
     q_out (M, N) uint8 and s_out (N/128, M) float32 (BLOCKWISE): also receive the 1x128
     rowwise quantization of the BF16 C, made in the GEMM's epilogue.
@@ -475,6 +618,10 @@ def gemm(a, b, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, a_scale=None, b_scale=N
     that a mostly idle last wave is split into K ranges."""
     args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
                          out, accumulate_fp32, a_format, b_format, q_out, s_out)
+    if m_offsets is not None:
+        with _on(a.device, stream):
+            _check(fp8q_gemm_blockscaled(args, _stream(stream)), "fp8q_gemm_blockscaled")
+        return c
     ws = None
     if split_tail and recipe == FP8Q_BLOCKWISE:
         nbytes = fp8q_gemm_workspace_bytes(args)
@@ -499,6 +646,134 @@ def gemm_workspace_bytes(M, N, K, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, accu
     if fused_quant:
         args.q_out, args.s_out = 16, 16          # only their presence is read
     return fp8q_gemm_workspace_bytes(args)
+
+
+_DTYPES = {torch.bfloat16: FP8Q_BF16, torch.float32: FP8Q_FP32}
+
+
+def _norm_operands(y, h, w_pre, w_post, gate, like_y=(), like_h=(), rows=()):
+    """Checks the tensors of a norm call; returns (h_dtype, w_dtype).  like_y / like_h: further matrices of y's
+    type and of h's; rows: float32 vectors with one value per row."""
+    _check_bf16(y, "y")
+    R, C = y.shape
+    if h.dtype not in _DTYPES or w_pre.dtype not in _DTYPES:
+        raise ValueError("h and the weights must be bfloat16 or float32")
+    for t in (h, *like_y, *like_h):
+        if t.shape != y.shape or t.device != y.device or (C > 1 and t.stride(1) != 1):
+            raise ValueError("matrices must be row-major, of y's shape and on its device")
+    if any(t.dtype != torch.bfloat16 for t in like_y) or any(t.dtype != h.dtype for t in like_h):
+        raise ValueError("matrices of y's kind must be bfloat16, those of h's kind of h's type")
+    for t in (w_pre, w_post, gate):
+        if t is not None and (t.dtype != w_pre.dtype or t.device != y.device or tuple(t.shape) != (C,)
+                              or not t.is_contiguous()):
+            raise ValueError("w_pre, w_post and gate must be contiguous vectors of y's columns, of one type")
+    for t in rows:
+        if t.dtype != torch.float32 or t.device != y.device or tuple(t.shape) != (R,) or not t.is_contiguous():
+            raise ValueError("rstd vectors must be contiguous float32, one value per row")
+    return _DTYPES[h.dtype], _DTYPES[w_pre.dtype]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, normed=True, quantize=False, out=None,
+                  stream=None):
+    """h' = alpha h + gate * norm(y) * w_post (without w_post: the plain y; without gate: 1) and the next block's
+    norm n = norm(h') * w_pre, RMS norms over the columns, in one pass.  y (R, C) bfloat16; h (R, C) bfloat16 or
+    float32; w_pre, w_post, gate (C,) bfloat16 or float32, all of one type.  Returns h (h', h's type; written to
+    `out` if given, which may be h itself), n (R, C) bfloat16 if `normed`, q_row and s_row (the 1x128
+    quantization of n, laid out as quantize_1x128 does) if `quantize`, and rstd_pre, rstd_post (R,) float32 for
+    norm_residual_backward (rstd_post None without w_post)."""
+    h_out = torch.empty_like(h, memory_format=torch.contiguous_format) if out is None else out
+    hd, wd = _norm_operands(y, h, w_pre, w_post, gate, like_h=(h_out,))
+    if not (normed or quantize):
+        raise ValueError("neither output of the norm is asked for")
+    R, C = y.shape
+    dev = y.device
+    o = {"h": h_out, "rstd_pre": torch.empty((R,), dtype=torch.float32, device=dev),
+         "rstd_post": None if w_post is None else torch.empty((R,), dtype=torch.float32, device=dev)}
+    if normed:
+        o["n"] = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+    if quantize:
+        o["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        o["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
+    a = NormArgs(R, C, hd, wd, alpha, eps, y.data_ptr(), _ld(y), h.data_ptr(), _ld(h), _addr(w_post), _addr(gate),
+                 w_pre.data_ptr(), h_out.data_ptr(), _ld(h_out), _addr(o.get("n")), C, _addr(o.get("q_row")),
+                 _addr(o.get("s_row")), o["s_row"].shape[1] if quantize else 0, _addr(o["rstd_post"]),
+                 o["rstd_pre"].data_ptr())
+    with _on(dev, stream):
+        _check(fp8q_norm_residual(a, _stream(stream)), "fp8q_norm_residual")
+    return o
+
+
+def _ld(t):
+    """Row stride of a row-major matrix; a single row has the columns' (its own stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post=None, gate=None, alpha=1.0,
+                           stream=None):
+    """Gradients of norm_residual from dn (of n, bfloat16) and dh (of h', of h's type); y, w_pre, w_post, gate and
+    alpha as given to it, h, rstd_pre and rstd_post as it returned them.  Returns dh (of the incoming residual),
+    dy (bfloat16), and float32 dw_pre, with w_post dw_post, with gate dgate (C,)."""
+    if (w_post is None) != (rstd_post is None):
+        raise ValueError("w_post and rstd_post go together")
+    hd, wd = _norm_operands(y, h, w_pre, w_post, gate, like_y=(dn,), like_h=(dh,),
+                            rows=(rstd_pre,) if rstd_post is None else (rstd_pre, rstd_post))
+    R, C = y.shape
+    dev = y.device
+    vec = lambda: torch.empty((C,), dtype=torch.float32, device=dev)  # noqa: E731
+    o = {"dh": torch.empty((R, C), dtype=h.dtype, device=dev), "dy": torch.empty((R, C), dtype=torch.bfloat16, device=dev),
+         "dw_pre": vec()}
+    if w_post is not None:
+        o["dw_post"] = vec()
+    if gate is not None:
+        o["dgate"] = vec()
+    with _on(dev, stream):
+        nbytes = fp8q_norm_backward_workspace_bytes(R, C, hd)
+        ws = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
+        a = NormBackwardArgs(R, C, hd, wd, alpha, dn.data_ptr(), _ld(dn), dh.data_ptr(), _ld(dh), y.data_ptr(), _ld(y),
+                             h.data_ptr(), _ld(h), _addr(w_post), _addr(gate), w_pre.data_ptr(), _addr(rstd_post),
+                             rstd_pre.data_ptr(), o["dh"].data_ptr(), C, o["dy"].data_ptr(), C, _addr(o.get("dw_post")),
+                             _addr(o.get("dgate")), o["dw_pre"].data_ptr(), ws.data_ptr(), nbytes)
+        _check(fp8q_norm_residual_backward(a, _stream(stream)), "fp8q_norm_residual_backward")
+    return o
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
+    """Global L2 norm of a list of contiguous CUDA gradients (bfloat16 and float32, any shapes and sizes), and
+    clipping by it: every gradient times min(1, max_norm / (norm + eps)), in place or into the tensors of the list
+    `out` (same types and sizes; no overlap with other tensors).  Returns the norm before clipping as a float32
+    CUDA tensor of shape () (nothing is read on the host)."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("no gradients")
+    if len(outs) != len(grads):
+        raise ValueError("out must have one tensor per gradient")
+    dev = grads[0].device
+    flat = []
+    for g, o in zip(grads, outs):
+        dt = _DTYPES.get(g.dtype)
+        if dt is None or g.device != dev or not g.is_cuda or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
+        n = g.numel()
+        if o is not g and (o.dtype != g.dtype or o.device != dev or o.numel() != n or not o.is_contiguous()):
+            raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
+        flat += (g.data_ptr(), o.data_ptr(), n, dt)
+    items = (ctypes.c_int64 * len(flat))(*flat)        # GradItem is four 64-bit words
+    nbytes = fp8q_clip_grad_workspace_bytes(len(grads))
+    ws = torch.empty(nbytes + 16, dtype=torch.uint8, device=dev)     # the norm after the partial sums
+    norm = ws[nbytes:nbytes + 4].view(torch.float32)[0]
+    if stream is not None:
+        ws.record_stream(stream)
+    with _on(dev, stream):
+        st = fp8q_clip_grad_norm(items, len(grads), max_norm, eps, _ptr(norm), _ptr(ws), nbytes, _stream(stream))
+    _check(st, "fp8q_clip_grad_norm")
+    return norm
 
 
 def device_status(stream=None):

@@ -3,10 +3,14 @@
 // either enqueues its kernels on the caller's stream or returns an error without launching.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "../../include/fp8q.h"
 #include "kernels.h"
@@ -294,6 +298,37 @@ fp8q_status fp8q_quantize_128x128_grouped(const void* w, int64_t groups, int64_t
                                      static_cast<cudaStream_t>(stream)));
 }
 
+int64_t fp8q_grouped_capacity(int64_t rows, int32_t groups) {
+  if (rows <= 0 || groups <= 0) return 0;
+  const int64_t bands = rows / 128 + groups;
+  return 128 * (bands < rows ? bands : rows);
+}
+
+fp8q_status fp8q_quantize_1x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                        const int32_t* offsets, int32_t groups, uint8_t* q_row, float* s_row,
+                                        int64_t ld_s_row, uint8_t* q_col, float* s_col, int64_t ld_s_col,
+                                        void* stream) {
+  fp8q_status st = check_input(x, rows, cols, ld_x);
+  if (st != FP8Q_OK) return st;
+  if (groups < 1) return FP8Q_ERR_SHAPE;
+  if (groups > 256) return FP8Q_ERR_UNSUPPORTED;
+  const bool row = q_row || s_row;
+  if (!offsets || !q_col || !s_col || (row && (!q_row || !s_row))) return FP8Q_ERR_NULL;
+  if (row && (cols % 128 != 0 || ld_s_row < rows || ld_s_row % 4 != 0)) return FP8Q_ERR_SHAPE;
+  if (cols % 16 != 0 || ld_s_col < cols || ld_s_col % 4 != 0) return FP8Q_ERR_SHAPE;
+  if ((row && !aligned16(q_row)) || !aligned16(q_col)) return FP8Q_ERR_ALIGN;
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  const int64_t bands = fp8q_grouped_capacity(rows, groups) / 128;
+  TileQuantParams p{static_cast<const uint16_t*>(x), rows, cols, ld_x, q_row, s_row, ld_s_row,
+                    q_col, s_col, ld_s_col, (int)((cols + 127) / 128), 0};
+  if (bands * p.tiles_c >= (1ll << 31)) return FP8Q_ERR_SHAPE;
+  DeviceScratch* d = nullptr;
+  if ((st = scratch(&d)) != FP8Q_OK) return st;
+  return from_cuda(launch_tile_quant_grouped(row, p, offsets, groups, bands, d->num_sms,
+                                             d->base.load(std::memory_order_acquire),
+                                             static_cast<cudaStream_t>(stream)));
+}
+
 fp8q_status fp8q_quantize_mx32(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q_row,
                                uint8_t* e8m0_row, uint8_t* q_col, uint8_t* e8m0_col, fp8q_sf_layout sf_layout,
                                void* stream) {
@@ -441,6 +476,238 @@ fp8q_status fp4q_quantize_2d16(const void* x, int64_t rows, int64_t cols, int64_
   return from_cuda(launch_fp4_quant_2d(p, tiles_of(rows, cols), s));
 }
 
+// ------------------------------------------------------------------ norms around a block
+static bool norm_dims_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && rows < (1ll << 31) && cols >= 8 && cols <= 16384 && cols % 8 == 0;
+}
+static bool norm_ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld % 8 == 0; }
+static bool is_dtype(int32_t d) { return d == FP8Q_BF16 || d == FP8Q_FP32; }
+
+fp8q_status fp8q_norm_residual(const fp8q_norm_args* a, void* stream) {
+  if (!a) return FP8Q_ERR_NULL;
+  if (!is_dtype(a->h_dtype) || !is_dtype(a->w_dtype)) return FP8Q_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(a->rows, a->cols) || !(a->eps >= 0.0f) || std::isinf(a->eps)) return FP8Q_ERR_SHAPE;
+  if (a->rows == 0) return FP8Q_OK;
+  const bool quant = a->q_row || a->s_row;
+  if (quant && (!a->q_row || !a->s_row)) return FP8Q_ERR_NULL;
+  if (!a->n_out && !quant) return FP8Q_ERR_NULL;
+  if (quant && (a->cols % 128 != 0 || a->ld_s_row < a->rows || a->ld_s_row % 4 != 0)) return FP8Q_ERR_SHAPE;
+  if (!norm_ld_ok(a->ld_y, a->cols) || !norm_ld_ok(a->ld_h, a->cols) || !norm_ld_ok(a->ld_h_out, a->cols) ||
+      (a->n_out && !norm_ld_ok(a->ld_n, a->cols)))
+    return FP8Q_ERR_SHAPE;
+  if (!a->y || !a->h || !a->h_out || !a->w_pre) return FP8Q_ERR_NULL;
+  for (const void* p : {a->y, a->h, a->w_post, a->gate, a->w_pre, (const void*)a->h_out, (const void*)a->n_out,
+                        (const void*)a->q_row})
+    if (!aligned16(p)) return FP8Q_ERR_ALIGN;
+  DeviceScratch* d = nullptr;
+  const fp8q_status st = scratch(&d);
+  if (st != FP8Q_OK) return st;
+  NormParams p{};
+  p.rows = a->rows;
+  p.cols = (int)a->cols;
+  p.alpha = a->alpha;
+  p.eps = a->eps;
+  p.y = a->y;
+  p.ld_y = a->ld_y;
+  p.h = a->h;
+  p.ld_h = a->ld_h;
+  p.w_post = a->w_post;
+  p.gate = a->gate;
+  p.w_pre = a->w_pre;
+  p.h_out = a->h_out;
+  p.ld_h_out = a->ld_h_out;
+  p.n_out = a->n_out;
+  p.ld_n = a->ld_n;
+  p.q_row = a->q_row;
+  p.s_row = a->s_row;
+  p.ld_s_row = a->ld_s_row;
+  p.rstd_post = a->rstd_post;
+  p.rstd_pre = a->rstd_pre;
+  p.status = d->base.load(std::memory_order_acquire);
+  return from_cuda(launch_norm_forward(p, a->h_dtype == FP8Q_FP32, a->w_dtype == FP8Q_FP32, d->num_sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8q_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t h_dtype) {
+  if (!norm_dims_ok(rows, cols) || !is_dtype(h_dtype)) return 0;
+  DeviceScratch* d = nullptr;
+  if (scratch(&d) != FP8Q_OK) return 0;
+  const int ctas = rows == 0 ? 1 : norm_backward_ctas(rows, (int)cols, h_dtype == FP8Q_FP32, d->num_sms);
+  return (size_t)ctas * 2 * (size_t)cols * sizeof(float);
+}
+
+fp8q_status fp8q_norm_residual_backward(const fp8q_norm_backward_args* a, void* stream) {
+  if (!a) return FP8Q_ERR_NULL;
+  if (!is_dtype(a->h_dtype) || !is_dtype(a->w_dtype)) return FP8Q_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(a->rows, a->cols)) return FP8Q_ERR_SHAPE;
+  for (int64_t ld : {a->ld_dn, a->ld_dh_out, a->ld_y, a->ld_h, a->ld_dh, a->ld_dy})
+    if (!norm_ld_ok(ld, a->cols)) return FP8Q_ERR_SHAPE;
+  if (!a->w_pre || !a->dw_pre || !a->workspace) return FP8Q_ERR_NULL;
+  if ((a->dw_post && !a->w_post) || (a->dgate && !a->gate)) return FP8Q_ERR_NULL;
+  if (a->rows > 0 && (!a->dn || !a->dh_out || !a->y || !a->h || !a->dh || !a->dy || !a->rstd_pre ||
+                      (a->w_post && !a->rstd_post)))
+    return FP8Q_ERR_NULL;
+  for (const void* p : {a->dn, a->dh_out, a->y, a->h, a->w_post, a->gate, a->w_pre, (const void*)a->dh,
+                        (const void*)a->dy, (const void*)a->workspace})
+    if (!aligned16(p)) return FP8Q_ERR_ALIGN;
+  DeviceScratch* d = nullptr;
+  const fp8q_status st = scratch(&d);
+  if (st != FP8Q_OK) return st;
+  if (a->workspace_bytes < 0 ||
+      (size_t)a->workspace_bytes < fp8q_norm_backward_workspace_bytes(a->rows, a->cols, a->h_dtype))
+    return FP8Q_ERR_SHAPE;
+  NormParams p{};
+  p.rows = a->rows;
+  p.cols = (int)a->cols;
+  p.alpha = a->alpha;
+  p.dn = a->dn;
+  p.ld_dn = a->ld_dn;
+  p.dh_in = a->dh_out;
+  p.ld_dh_in = a->ld_dh_out;
+  p.y = a->y;
+  p.ld_y = a->ld_y;
+  p.h = a->h;
+  p.ld_h = a->ld_h;
+  p.w_post = a->w_post;
+  p.gate = a->gate;
+  p.w_pre = a->w_pre;
+  p.rstd_post = const_cast<float*>(a->rstd_post);
+  p.rstd_pre = const_cast<float*>(a->rstd_pre);
+  p.dh = a->dh;
+  p.ld_dh = a->ld_dh;
+  p.dy = a->dy;
+  p.ld_dy = a->ld_dy;
+  p.dw_post = a->dw_post;
+  p.dgate = a->dgate;
+  p.dw_pre = a->dw_pre;
+  p.partials = static_cast<float*>(a->workspace);
+  p.status = d->base.load(std::memory_order_acquire);
+  return from_cuda(launch_norm_backward(p, a->h_dtype == FP8Q_FP32, a->w_dtype == FP8Q_FP32, d->num_sms,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ gradient clipping
+}  // extern "C"
+
+namespace {
+
+constexpr int kClipCtas = 592;   // most CTAs (FP64 partials) of one norm launch: 4 per SM of 148
+
+struct ByteRange {
+  uintptr_t begin, end;
+};
+
+// Whether some item's out overlaps another item's out, or a grad that is not its own.
+bool clip_overlaps(const fp8q_grad_item* items, int64_t n, ByteRange* outs) {
+  int64_t k = 0;
+  auto range = [](const void* p, const fp8q_grad_item& it) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return ByteRange{b, b + (uintptr_t)it.numel * (it.dtype == FP8Q_FP32 ? 4u : 2u)};
+  };
+  for (int64_t i = 0; i < n; ++i)
+    if (items[i].numel > 0) outs[k++] = range(items[i].out, items[i]);
+  std::sort(outs, outs + k, [](const ByteRange& a, const ByteRange& b) { return a.begin < b.begin; });
+  for (int64_t i = 1; i < k; ++i)
+    if (outs[i].begin < outs[i - 1].end) return true;
+  for (int64_t i = 0; i < n; ++i) {
+    if (items[i].numel == 0) continue;
+    const ByteRange g = range(items[i].grad, items[i]);
+    const ByteRange* o = std::upper_bound(outs, outs + k, g.begin,
+                                          [](uintptr_t v, const ByteRange& r) { return v < r.end; });
+    if (o == outs + k || o->begin >= g.end) continue;                     // nothing written there
+    if (items[i].grad != items[i].out || o->begin != g.begin) return true;
+  }
+  return false;
+}
+
+// Runs `f` on the items' launches: f(tensors, batch) with up to 1024 items each.
+template <int MAX, class F>
+fp8q_status clip_batches(const fp8q_grad_item* items, int64_t n, F f) {
+  std::unique_ptr<ClipTensors<MAX>> t(new (std::nothrow) ClipTensors<MAX>);
+  if (!t) return FP8Q_ERR_CUDA;
+  int64_t i = 0;
+  for (int batch = 0; i < n || batch == 0; ++batch) {
+    t->n = 0;
+    int64_t chunks = 0;
+    for (; i < n && t->n < MAX; ++i) {
+      const fp8q_grad_item& it = items[i];
+      if (it.numel == 0) continue;
+      const int64_t bytes = it.numel * (it.dtype == FP8Q_FP32 ? 4 : 2);
+      t->chunk_begin[t->n] = (int)chunks;
+      t->grad[t->n] = it.grad;
+      t->out[t->n] = it.out;
+      t->numel[t->n] = it.dtype == FP8Q_FP32 ? -it.numel : it.numel;
+      ++t->n;
+      chunks += clip_chunks(it.grad, bytes);
+      if (chunks >= (1ll << 30)) return FP8Q_ERR_SHAPE;
+    }
+    t->chunk_begin[t->n] = (int)chunks;
+    const cudaError_t e = f(*t, batch, (int)chunks);
+    if (e != cudaSuccess) return FP8Q_ERR_CUDA;
+  }
+  return FP8Q_OK;
+}
+
+template <int MAX>
+fp8q_status clip_run(const fp8q_grad_item* items, int64_t n, double max_norm, double eps, float* norm, double* ws,
+                     int ctas, cudaStream_t s) {
+  bool in_place = true;
+  int n_partials = 0;
+  for (int64_t i = 0; i < n; ++i) in_place &= items[i].numel == 0 || items[i].grad == items[i].out;
+  fp8q_status st = clip_batches<MAX>(items, n, [&](const ClipTensors<MAX>& t, int, int chunks) {
+    const int grid = std::max(1, std::min(chunks, ctas));
+    const cudaError_t e = launch_clip_norm<MAX>(t, ws + n_partials, grid, s);
+    n_partials += grid;
+    return e;
+  });
+  if (st != FP8Q_OK) return st;
+  return clip_batches<MAX>(items, n, [&](const ClipTensors<MAX>& t, int batch, int chunks) {
+    return launch_clip_scale<MAX>(t, ws, n_partials, max_norm, eps, batch == 0 ? norm : nullptr, in_place,
+                                  std::max(1, std::min(chunks, ctas)), s);
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp8q_clip_grad_workspace_bytes(int64_t n_items) {
+  if (n_items < 0) return 0;
+  return (size_t)std::max<int64_t>(1, (n_items + kClipMany - 1) / kClipMany) * kClipCtas * sizeof(double);
+}
+
+fp8q_status fp8q_clip_grad_norm(const fp8q_grad_item* items, int64_t n_items, double max_norm, double eps,
+                                float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (n_items < 0 || n_items > (1 << 20)) return FP8Q_ERR_SHAPE;
+  if (n_items > 0 && !items) return FP8Q_ERR_NULL;
+  if (!(max_norm >= 0.0) || !(eps >= 0.0) || std::isinf(eps)) return FP8Q_ERR_SHAPE;
+  for (int64_t i = 0; i < n_items; ++i) {
+    const fp8q_grad_item& it = items[i];
+    if (it.dtype != FP8Q_BF16 && it.dtype != FP8Q_FP32) return FP8Q_ERR_UNSUPPORTED;
+    if (it.numel < 0 || it.numel >= (1ll << 40)) return FP8Q_ERR_SHAPE;
+    if (it.numel == 0) continue;
+    if (!it.grad || !it.out) return FP8Q_ERR_NULL;
+    const uintptr_t m = it.dtype == FP8Q_FP32 ? 3 : 1;
+    if ((reinterpret_cast<uintptr_t>(it.grad) & m) || (reinterpret_cast<uintptr_t>(it.out) & m)) return FP8Q_ERR_ALIGN;
+  }
+  if (!workspace) return FP8Q_ERR_NULL;
+  if (!aligned16(workspace)) return FP8Q_ERR_ALIGN;
+  if (workspace_bytes < 0 || (size_t)workspace_bytes < fp8q_clip_grad_workspace_bytes(n_items)) return FP8Q_ERR_SHAPE;
+  {
+    std::unique_ptr<ByteRange[]> outs(new (std::nothrow) ByteRange[n_items + 1]);
+    if (!outs) return FP8Q_ERR_CUDA;
+    if (clip_overlaps(items, n_items, outs.get())) return FP8Q_ERR_UNSUPPORTED;
+  }
+  DeviceScratch* d = nullptr;
+  const fp8q_status st = scratch(&d);
+  if (st != FP8Q_OK) return st;
+  const int ctas = std::min(kClipCtas, 4 * d->num_sms);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  double* ws = static_cast<double*>(workspace);
+  return n_items <= kClipFew ? clip_run<kClipFew>(items, n_items, max_norm, eps, norm, ws, ctas, s)
+                             : clip_run<kClipMany>(items, n_items, max_norm, eps, norm, ws, ctas, s);
+}
+
 // ------------------------------------------------------------------ GEMM
 fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   if (!a) return FP8Q_ERR_NULL;
@@ -467,7 +734,8 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->K == 0) {  // empty sum: C = 0, or C unchanged when accumulating
     if (acc32) return FP8Q_OK;
-    return from_cuda(cudaMemset2DAsync(a->c, (size_t)a->ldc * 2, 0, (size_t)a->N * 2, (size_t)a->M, s));
+    const size_t c_rows = (size_t)a->M * (a->num_groups > 0 && a->layout == FP8Q_WGRAD ? (size_t)a->num_groups : 1);
+    return from_cuda(cudaMemset2DAsync(a->c, (size_t)a->ldc * 2, 0, (size_t)a->N * 2, c_rows, s));
   }
   const bool fp4 = a->recipe == FP8Q_NVFP4;
   const int64_t kbytes = fp4 ? a->K / 2 : a->K;
@@ -478,10 +746,13 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   const bool grouped = a->num_groups > 0;
   if (a->num_groups < 0) return FP8Q_ERR_SHAPE;
   if (grouped) {
-    if (a->recipe != FP8Q_BLOCKWISE || a->layout != FP8Q_FPROP) return FP8Q_ERR_UNSUPPORTED;
+    if (a->recipe != FP8Q_BLOCKWISE) return FP8Q_ERR_UNSUPPORTED;
     if (a->num_groups > 256) return FP8Q_ERR_UNSUPPORTED;
     if (!a->m_offsets) return FP8Q_ERR_NULL;
+    // rows of the stacked C (wgrad) or B (fprop, dgrad) are 32-bit coordinates
+    if ((int64_t)a->num_groups * (a->layout == FP8Q_WGRAD ? a->M : a->N) >= (1ll << 31)) return FP8Q_ERR_SHAPE;
   }
+  const bool k_groups = grouped && a->layout == FP8Q_WGRAD;   // experts split K and stack C
   GemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.recipe = a->recipe;
@@ -540,7 +811,8 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   p.status = d->base.load(std::memory_order_acquire);
 
   CUtensorMap ma, mb, msb;
-  const int64_t b_rows = grouped ? (int64_t)a->num_groups * a->N : a->N;
+  const int64_t b_rows = grouped && !k_groups ? (int64_t)a->num_groups * a->N : a->N;
+  const int64_t c_rows = k_groups ? (int64_t)a->num_groups * a->M : a->M;
   if (!make_map(&ma, a->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, kbytes, a->M, a->lda, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_128B))
     return FP8Q_ERR_CUDA;
@@ -563,11 +835,11 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   CUtensorMap mc = ma, mq = ma;
   if (a->recipe == FP8Q_BLOCKWISE && acc32 && a->M > 0 && a->N > 0) {
     // FP32 accumulation: 32 x 16 FP32 boxes added into C by TMA reduction
-    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a->N, a->M, a->ldc * 4, 16, 32,
+    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a->N, c_rows, a->ldc * 4, 16, 32,
                   CU_TENSOR_MAP_SWIZZLE_64B))
       return FP8Q_ERR_CUDA;
   } else if (a->recipe == FP8Q_BLOCKWISE && a->M > 0 && a->N > 0) {
-    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->N, a->M, a->ldc * 2, 32, 32,
+    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->N, c_rows, a->ldc * 2, 32, 32,
                   CU_TENSOR_MAP_SWIZZLE_64B))
       return FP8Q_ERR_CUDA;
     if (qout && !make_map(&mq, a->q_out, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->N, a->M, a->ld_q_out, 64, 32,

@@ -578,15 +578,25 @@ struct BwSmem {
 };
 
 // Pair tile t: 256 rows x BN columns, rasterized like tile_of; grouped GEMMs enumerate each
-// expert's 256-row tiles.  Returns this CTA's 128-row half.
-template <int BN>
+// expert's 256-row tiles.  KGROUP (grouped wgrad): every expert has the same tile grid, one
+// expert after the other.  Returns this CTA's 128-row half.
+template <int BN, bool KGROUP = false>
 __device__ __forceinline__ Tile pair_tile_of(int t, const GemmParams& p, int row_tiles, const int* prefix,
                                              const int* offs, uint32_t rank) {
   int rt, nt;
-  raster_pos(t, p, row_tiles, rt, nt);
   Tile T;
-  T.n0 = nt * BN;
   int end;
+  if constexpr (KGROUP) {
+    const int per = row_tiles * p.tiles_n;
+    T.g = t / per;
+    raster_pos(t - T.g * per, p, row_tiles, rt, nt);
+    T.n0 = nt * BN;
+    T.m0 = rt * kBwPairM + (int)rank * kBM;
+    T.mend = min(p.M, T.m0 + kBM);
+    return T;
+  }
+  raster_pos(t, p, row_tiles, rt, nt);
+  T.n0 = nt * BN;
   if (p.num_groups > 0) {
     int g = 0;
     while (g + 1 < p.num_groups && prefix[g + 1] <= rt) ++g;
@@ -626,6 +636,31 @@ __device__ __forceinline__ void load_pair_groups(const GemmParams& p, int* prefi
   }
 }
 
+// Grouped wgrad: expert g's tokens are chunks [prefix[g], prefix[g + 1]) of the operands' K
+// axis, ceil(tokens / 128) of them (the layout of the grouped 1x128 quantizer).  Offsets that
+// decrease, or whose chunks would pass the KB chunks of K, are clamped (and recorded), so no
+// chunk outside the operands is read.
+__device__ __forceinline__ void load_chunk_groups(const GemmParams& p, int KB, int* prefix, int* offs, int lane) {
+  for (int g = lane; g <= p.num_groups; g += 32) offs[g] = p.m_offsets[g];
+  __syncwarp();
+  if (lane == 0) {
+    int64_t prev = offs[0];
+    bool bad = prev != 0;
+    int acc = 0;
+    for (int g = 0; g < p.num_groups; ++g) {
+      prefix[g] = acc;
+      const int64_t v = offs[g + 1], c = (v - prev + kBKB - 1) / kBKB;
+      bad |= v < prev || c > KB - acc;
+      if (v > prev) {
+        acc += (int)min(c, (int64_t)(KB - acc));
+        prev = v;
+      }
+    }
+    prefix[p.num_groups] = acc;
+    if (bad && blockIdx.x == 0) atomicExch(p.status, kDevBadArg);
+  }
+}
+
 // Work unit t of a launch: the raster index of its pair tile and its K chunks [kb0, kb1).
 // Units below main_tiles are whole tiles; with a split last wave, unit main_tiles + u is K
 // range u % tail_splits of tile main_tiles + u / tail_splits.
@@ -657,6 +692,9 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
   // BF16 output or FP32 accumulation, not grouped: the last wave may be split into K ranges,
   // whose FP32 partial sums go to the workspace (p.ws, through tma_q) instead of C
   constexpr bool RANGES = (EPI == kEpiBf16 || EPI == kEpiAcc32) && !GROUPED;
+  // grouped wgrad: experts share the output shape and split the K axis (ragged K); grouped
+  // fprop and dgrad: experts split the rows (ragged M)
+  constexpr bool KGROUP = GROUPED && kWg;
   using C = BwCfg<L>;
   constexpr int kBwBN = C::BN, kBwHalfBN = C::HalfBN, kBwEpiWarps = C::EpiWarps;
   constexpr int kBwProducerWarp = C::ProducerWarp, kBwMmaWarp = C::MmaWarp;
@@ -700,7 +738,10 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
     mbar_arrive_count(&go[0], 2 * kBwEpiWarps);
     mbar_arrive_count(&go[1], 2 * kBwEpiWarps);
   }
-  if (GROUPED && warp == kBwProducerWarp) load_pair_groups(p, prefix, offs, lane);
+  if (GROUPED && warp == kBwProducerWarp) {
+    if constexpr (KGROUP) load_chunk_groups(p, KB, prefix, offs, lane);
+    else load_pair_groups(p, prefix, offs, lane);
+  }
   if (warp == kBwMmaWarp) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
@@ -710,11 +751,21 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
   cluster_sync();   // barriers and TMEM of both CTAs exist before either CTA uses them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int row_tiles = GROUPED ? prefix[p.num_groups] : p.tiles_m;
-  const int total = GROUPED ? row_tiles * p.tiles_n
+  const int row_tiles = GROUPED && !KGROUP ? prefix[p.num_groups] : p.tiles_m;
+  const int total = KGROUP ? p.num_groups * row_tiles * p.tiles_n
+                    : GROUPED ? row_tiles * p.tiles_n
                     : RANGES ? p.main_tiles + (p.tiles_m * p.tiles_n - p.main_tiles) * p.tail_splits
                              : p.main_tiles;
   const int cluster = (int)(blockIdx.x >> 1), n_clusters = (int)(gridDim.x >> 1);
+  auto chunks_of = [&](int t, int& kb0, int& kb1) {
+    if constexpr (KGROUP) {
+      const int g = t / (row_tiles * p.tiles_n);
+      kb0 = prefix[g];
+      kb1 = prefix[g + 1];
+    } else {
+      unit_chunks<RANGES>(t, p, KB, kb0, kb1);
+    }
+  };
 
   if (warp >= kBwEpiWarps) {
   // wgrad: the helper warpgroup (warps 16-19) gives registers to the promotion warps
@@ -729,10 +780,10 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += n_clusters) {
-        const Tile T = pair_tile_of<kBwBN>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
-        const int b_row = T.g * p.N + T.n0 + (int)rank * kBwHalfBN;
+        const Tile T = pair_tile_of<kBwBN, KGROUP>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
+        const int b_row = (KGROUP ? 0 : T.g * p.N) + T.n0 + (int)rank * kBwHalfBN;
         int kb0, kb1;
-        unit_chunks<RANGES>(t, p, KB, kb0, kb1);
+        chunks_of(t, kb0, kb1);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const uint32_t s = it % kStages, ph = (it / kStages) & 1;
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, kWaitLimitNs)) {
@@ -764,10 +815,12 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int t = cluster; t < total && ok; t += n_clusters) {
-      const Tile T = pair_tile_of<kBwBN>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
-      const float* sbg = p.sb + (GROUPED ? (int64_t)T.g * ((p.N + kBM - 1) / kBM) * p.ld_sb : 0);
+      const Tile T = pair_tile_of<kBwBN, KGROUP>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
+      // an expert's B scales: [N/128][K/128] (fprop) or [K/128][N/128] (dgrad)
+      const float* sbg = p.sb + (GROUPED && !KGROUP
+                                     ? (int64_t)T.g * (L == kFprop ? (p.N + kBM - 1) / kBM : KB) * p.ld_sb : 0);
       int kb0, kb1;
-      unit_chunks<RANGES>(t, p, KB, kb0, kb1);
+      chunks_of(t, kb0, kb1);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t r = it % kBwSb, rph = (it / kBwSb) & 1;
         int good = 1;
@@ -813,7 +866,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
       bool ok = true;
       for (int t = cluster; t < total && ok; t += n_clusters) {
         int kb0, kb1;
-        unit_chunks<RANGES>(t, p, KB, kb0, kb1);
+        chunks_of(t, kb0, kb1);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const uint32_t s = it % kStages, pb = it & 1;
           if (!mbar_wait(&go[it % kBwGo], (it / kBwGo) & 1, abort_flag, kWaitLimitNs)) {
@@ -846,13 +899,14 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
     uint32_t chunk = 0, tile_it = 0;
     bool ok = true;
     for (int t = cluster; t < total && ok; t += n_clusters, ++tile_it) {
-      const Tile T = pair_tile_of<kBwBN>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
+      const Tile T = pair_tile_of<kBwBN, KGROUP>(unit_tile<RANGES>(t, p), p, row_tiles, prefix, offs, rank);
       const int ncol0 = T.n0 + cgp * 64;
+      const int crow = KGROUP ? T.g * p.M : 0;   // the expert's first row of C
       float2 acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
       int kb0, kb1;
-      unit_chunks<RANGES>(t, p, KB, kb0, kb1);
+      chunks_of(t, kb0, kb1);
       for (int kb = kb0; kb < kb1; ++kb) {
         const uint32_t rs = chunk % kBwSb;
         if (!mbar_wait(&sfull[rs], (chunk / kBwSb) & 1, abort_flag, kWaitLimitNs)) { raise_timeout(p, abort_flag); ok = false; break; }
@@ -951,6 +1005,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
         }
         continue;
       }
+      if (KGROUP && ACC32 && kb0 == kb1) continue;   // an expert without tokens: C unchanged
       if constexpr (!ACC32) {
         // BF16: the staged 32 x 32 box goes out by one TMA store and the warp moves on to the
         // next tile while the copy engine writes it (the swizzled staging layout is the tensor
@@ -971,7 +1026,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tma_c, stg, ncol0 + h * EC, T.m0 + q * 32);
+              tma_store_2d(&tma_c, stg, ncol0 + h * EC, crow + T.m0 + q * 32);
               bulk_commit();
             }
             continue;
@@ -982,7 +1037,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
             const int r = i * RPI + lane / CPR, c = lane % CPR;
             const uint4 v = stg[r * CPR + (c ^ swz(r))];
             const int mr = T.m0 + q * 32 + r, n = ncol0 + h * EC + c * 8;
-            if (mr < T.mend && n < p.N) store8_bf16(p, mr, n, v);
+            if (mr < T.mend && n < p.N) store8_bf16(p, crow + mr, n, v);
           }
           __syncwarp();
         }
@@ -1006,7 +1061,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              tma_reduce_add_2d(&tma_c, stg, ncol0 + h * EC32, T.m0 + q * 32);
+              tma_reduce_add_2d(&tma_c, stg, ncol0 + h * EC32, crow + T.m0 + q * 32);
               bulk_commit();
             }
             continue;
@@ -1017,7 +1072,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
             const int r = i * RPI + lane / CPR, c = lane % CPR;
             const uint4 v = stg[r * CPR + (c ^ swz(r))];
             const int mr = T.m0 + q * 32 + r, n = ncol0 + h * EC32 + c * 4;
-            if (mr < T.mend && n < p.N) add4_f32(p, mr, n, v);
+            if (mr < T.mend && n < p.N) add4_f32(p, crow + mr, n, v);
           }
           __syncwarp();
         }
@@ -1143,7 +1198,7 @@ static cudaError_t blockwise_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute
 // Output tiles of a blockwise GEMM (256-row pair tiles x 256 columns) with its raster.
 static void blockwise_grid(GemmParams& q, bool grouped) {
   q.tiles_n = (q.N + kBlockwiseTileN - 1) / kBlockwiseTileN;
-  q.tiles_m = (q.M + kBwPairM - 1) / kBwPairM + (grouped ? q.num_groups : 0);
+  q.tiles_m = (q.M + kBwPairM - 1) / kBwPairM + (grouped && q.layout != kWgrad ? q.num_groups : 0);
   raster(q, q.tiles_m, kBwPairM, kBlockwiseTileN);
 }
 
@@ -1211,7 +1266,7 @@ static cudaError_t launch_blockwise(const GemmParams& p, const CUtensorMap& a, c
   if (e != cudaSuccess) return e;
   GemmParams q = p;
   blockwise_grid(q, G);
-  const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+  const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n * (G && L == kWgrad ? q.num_groups : 1);
   if (tiles > (int64_t)INT32_MAX / 2) return cudaErrorInvalidValue;
   q.main_tiles = (int)tiles;
   q.tail_splits = 0;
@@ -1305,7 +1360,11 @@ cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& tma_a, const CUt
                         const CUtensorMap& tma_ws, int num_sms, cudaStream_t s) {
   if (p.recipe == kBlockwise) {
     if (p.c32 != nullptr) {   // FP32 accumulate epilogue: its own instantiations
-      if (p.num_groups > 0) return launch_blockwise<kFprop, true, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+      if (p.num_groups > 0) {
+        if (p.layout == kFprop) return launch_blockwise<kFprop, true, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+        if (p.layout == kDgrad) return launch_blockwise<kDgrad, true, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+        return launch_blockwise<kWgrad, true, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+      }
       if (p.layout == kFprop) return launch_blockwise<kFprop, false, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
       if (p.layout == kDgrad) return launch_blockwise<kDgrad, false, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
       return launch_blockwise<kWgrad, false, kEpiAcc32>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
@@ -1315,7 +1374,11 @@ cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& tma_a, const CUt
       if (p.layout == kDgrad) return launch_blockwise<kDgrad, false, kEpiQuant>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
       return launch_blockwise<kWgrad, false, kEpiQuant>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
     }
-    if (p.num_groups > 0) return launch_blockwise<kFprop, true>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+    if (p.num_groups > 0) {
+      if (p.layout == kFprop) return launch_blockwise<kFprop, true>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+      if (p.layout == kDgrad) return launch_blockwise<kDgrad, true>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+      return launch_blockwise<kWgrad, true>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
+    }
     if (p.layout == kFprop) return launch_blockwise<kFprop, false>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
     if (p.layout == kDgrad) return launch_blockwise<kDgrad, false>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);
     return launch_blockwise<kWgrad, false>(p, tma_a, tma_b, tma_sb, tma_c, tma_q, tma_ws, num_sms, s);

@@ -42,6 +42,11 @@ struct TileQuantMulti {
 };
 cudaError_t launch_tile_quant_multi(const TileQuantMulti& m, int64_t tiles, cudaStream_t s);
 
+// 1x128 quantization grouped by expert (`groups` of them, row offsets on the device): the
+// transposed output has `bands` bands of 128 columns; codes of rows, if `row`, as ungrouped.
+cudaError_t launch_tile_quant_grouped(bool row, const TileQuantParams& p, const int32_t* offs, int groups,
+                                      int64_t bands, int num_sms, uint32_t* status, cudaStream_t s);
+
 // Per-tensor current scaling: amax pass into *amax_bits (zeroed by the caller), then cast.
 cudaError_t launch_tensor_amax(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x,
                                uint32_t* amax_bits, cudaStream_t s);
@@ -78,6 +83,54 @@ cudaError_t launch_fp4_quant(const Fp4QuantParams& p, int64_t tiles, cudaStream_
 // 16x16-block weight quantizer: global amax into amax_bits[0], then codes in the layouts
 // whose q pointer is set; g_row receives the decode scale.
 cudaError_t launch_fp4_quant_2d(const Fp4QuantParams& p, int64_t tiles, cudaStream_t s);
+
+// ------------------------------------------------------------------ gradient norm and clipping
+// Up to MAX tensors of one launch, passed by value (a launch of few tensors passes few bytes;
+// kernel parameters hold 32764 bytes): numel is negative for FP32, positive for BF16; tensor i
+// owns the launch's 16 KB chunks [chunk_begin[i], chunk_begin[i + 1]).
+constexpr int kClipFew = 64, kClipMany = 1024;
+template <int MAX>
+struct ClipTensors {
+  int n;
+  int chunk_begin[MAX + 1];
+  const void* grad[MAX];
+  void* out[MAX];
+  int64_t numel[MAX];
+};
+static_assert(sizeof(ClipTensors<kClipMany>) + 64 <= 32764, "kernel parameters");
+// Chunks of a tensor (its 16-byte aligned cover).
+int clip_chunks(const void* grad, int64_t bytes);
+// partials[0 .. grid): each CTA's sum of squares.
+template <int MAX>
+cudaError_t launch_clip_norm(const ClipTensors<MAX>& p, double* partials, int grid, cudaStream_t s);
+// norm = sqrt(sum of all partials) into norm_out (unless NULL), then out = min(1, max_norm /
+// (norm + eps)) * grad; in_place: every out is its grad.
+template <int MAX>
+cudaError_t launch_clip_scale(const ClipTensors<MAX>& p, const double* partials, int n_partials, double max_norm,
+                              double eps, float* norm_out, bool in_place, int grid, cudaStream_t s);
+
+// ------------------------------------------------------------------ norms around a block
+// Forward: y, h -> h_out, n_out and / or q_row, s_row; backward: dn, dh_in, y, h (the stored
+// h') -> dh, dy and the column sums.  Leading dimensions in elements.
+struct NormParams {
+  int64_t rows;
+  int cols, stages;   // stages: rows staged in shared memory (set by the launcher)
+  float alpha, eps;
+  const void *y, *h, *w_post, *gate, *w_pre, *dn, *dh_in;
+  int64_t ld_y, ld_h, ld_dn, ld_dh_in;
+  void *h_out, *n_out, *dh, *dy;
+  int64_t ld_h_out, ld_n, ld_dh, ld_dy;
+  uint8_t* q_row;
+  float* s_row;
+  int64_t ld_s_row;
+  float *rstd_post, *rstd_pre;
+  float *dw_pre, *dw_post, *dgate;
+  float* partials;    // [norm_backward_ctas][2][cols]
+  uint32_t* status;
+};
+int norm_backward_ctas(int64_t rows, int cols, bool h32, int num_sms);
+cudaError_t launch_norm_forward(const NormParams& p, bool h32, bool w32, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormParams& p, bool h32, bool w32, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ GEMM
 // Output tile width of the blockwise (FP32-promotion) kernel; the B and wgrad-scale TMA boxes

@@ -155,6 +155,32 @@ typedef struct fp8q_quant_item {
 } fp8q_quant_item;
 fp8q_status fp8q_quantize_multi(const fp8q_quant_item* items, int32_t n_items, void* stream);
 
+/* Rows of the padded token axis of fp8q_quantize_1x128_grouped for `rows` tokens of `groups`
+ * experts: 128 * min(rows / 128 + groups, rows), the most that the experts' token counts, each
+ * rounded up to a multiple of 128, can add up to (the counts themselves are on the device).
+ * A multiple of 128; 0 when rows or groups is not positive. */
+int64_t fp8q_grouped_capacity(int64_t rows, int32_t groups);
+
+/* [DSV3] "Fine-grained quantization" of a MoE layer's routed tokens, the weight-gradient operand:
+ * fp8q_quantize_1x128 with every 128-token tile inside one expert.  x: BF16 rows x cols, the
+ * tokens of expert 0, then those of expert 1 and so on; offsets (device int32[groups + 1],
+ * 1 <= groups <= 256): expert g's tokens are rows offsets[g] .. offsets[g + 1] - 1, with
+ * offsets[0] == 0, non-decreasing, offsets[groups] == rows.
+ * Colwise (required; cols % 16 == 0): expert g's tokens take ceil(tokens / 128) tiles on a padded
+ *   token axis of P = fp8q_grouped_capacity(rows, groups), one expert after the other;
+ *   q_col[c * P + t] (cols x P codes) and s_col[(t/128) * ld_s_col + c] (P/128 x cols decode
+ *   scales, ld_s_col >= cols, % 4 == 0).  Padding tokens, after an expert's last token and
+ *   after the last expert's tiles, count as zeros: code 0, and decode scale 1 for a tile without tokens.
+ *   These are the grouped WGRAD operands (fp8q_gemm_args).
+ * Rowwise (optional; cols % 128 == 0): q_row / s_row exactly as fp8q_quantize_1x128 writes them.
+ * x is read once for both.  The kernel reads the offsets on the device; offsets that break the
+ * rule are clamped to 0 .. rows and the status word records FP8Q_ERR_DEVICE_ARG.
+ * rows == 0 or cols == 0 -> FP8Q_OK, nothing launched. */
+fp8q_status fp8q_quantize_1x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                        const int32_t* offsets, int32_t groups,
+                                        uint8_t* q_row, float* s_row, int64_t ld_s_row,
+                                        uint8_t* q_col, float* s_col, int64_t ld_s_col, void* stream);
+
 /* [NeMo] MXFP8: 32-element blocks, E8M0 scale = smallest e with amax <= 448 * 2^e
  * (amax == 0 -> e = -127; e clamped to [-127, 127]; byte e + 127), codes
  * E4M3(fp32(x * 2^-e)).
@@ -279,14 +305,22 @@ fp8q_status fp4q_quantize_2d16(const void* x, int64_t rows, int64_t cols, int64_
  *   rule returns FP8Q_ERR_SHAPE.  K == 0 is allowed (C = 0, or unchanged when
  *   accumulating).
  * lda/ldb: row strides in bytes (% 16 == 0).  a/b 16-byte aligned.
- * Grouped (MoE, BLOCKWISE/FPROP only) when num_groups > 0: m_offsets[0..G] (device int32,
+ * Grouped (MoE, BLOCKWISE only) when num_groups = G > 0 (G <= 256); BF16 or FP32-accumulated C:
+ *   FPROP and DGRAD: m_offsets[0..G] (device int32,
  *   non-decreasing, m_offsets[0] == 0, m_offsets[G] == M) delimit each expert's rows of A
- *   and C; B is [G][N][K] (expert g at b + g * N * ldb) and b_scale [G][N/128][K/128]
- *   (expert g at g * (N/128) * ld_sb floats).  The kernel reads the offsets on the device
+ *   and C; B is [G][N][K] (expert g at b + g * N * ldb) and b_scale [G][ceil(N/128)][K/128]
+ *   (FPROP: expert g at g * ceil(N/128) * ld_sb floats) or [G][K/128][ceil(N/128)] (DGRAD:
+ *   expert g at g * (K/128) * ld_sb floats).  The kernel reads the offsets on the device
  *   and builds its tile schedule there (at most M/128 + G row tiles), so the host needs
  *   no copy of them.  Offsets that break the rule are clamped on the device to
  *   [previous offset, M] (no row outside C is ever written) and the device status word
  *   records FP8Q_ERR_DEVICE_ARG (read it with fp8q_get_device_status).
+ *   WGRAD: K is the padded token axis of fp8q_quantize_1x128_grouped (of X and of dY with the
+ *   same offsets), m_offsets[0..G] are the unpadded token offsets given to it, and expert g's
+ *   product runs over its own ceil(tokens / 128) chunks of 128 only: C is [G][M][N] (expert g at
+ *   c + g * M * ldc elements), the stacked weight gradients.  An expert without tokens gets
+ *   zeros (BF16 C) or keeps its C (c_fp32_accumulate).  Chunks that would pass K (offsets that
+ *   break the rule) are left out and the status word records FP8Q_ERR_DEVICE_ARG.
  * M, N >= 0 arbitrary (tails masked at the store).
  * c_fp32_accumulate (BLOCKWISE only; 0 for the other recipes): C is an FP32 row-major
  *   matrix (ldc % 4 == 0, c 16-byte aligned) that is updated in place,
@@ -345,6 +379,119 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* args, void* stream);
  * kernels enqueued on the call's stream; the caller must not use it concurrently elsewhere
  * before they complete.  Returns 0 for NULL or invalid arguments. */
 size_t fp8q_gemm_workspace_bytes(const fp8q_gemm_args* args);
+
+/* Element type of a tensor that may be either. */
+typedef enum { FP8Q_BF16 = 0, FP8Q_FP32 = 1 } fp8q_dtype;
+
+/* The norms on both sides of a block's residual connection, fused with its gate, the residual
+ * scale and the 1x128 quantization of what the next block's GEMM reads ([DSV3] "Online
+ * quantization"; "Mixed-precision framework": norms stay in high precision).  Per row of cols
+ * elements, in FP32, with rms(v) = 1 / sqrt(mean(v^2) + eps):
+ *   z  = y * rms(y) * w_post      (w_post NULL: z = y, no norm after the block)
+ *   h' = alpha * h + gate * z     (gate NULL: 1)
+ *   n  = h' * rms(h') * w_pre     (from h' before it is rounded)
+ * y: BF16 rows x cols, the block's output; h: the residual stream, rows x cols of h_dtype;
+ * w_pre, w_post, gate: cols values of w_dtype (fp8q_dtype).  Outputs: h_out (h_dtype; may be h),
+ * required; n_out (BF16) and / or q_row + s_row (1x128 codes and decode scales as
+ * fp8q_quantize_1x128 lays them out, cols % 128 == 0, ld_s_row >= rows, % 4 == 0, made from n in
+ * FP32), at least one; rstd_pre and rstd_post (rows floats: rms(h'), rms(y)), each optional.
+ * 1 <= cols <= 16384, cols % 8 == 0; leading dimensions (elements) >= cols, % 8 == 0; pointers of
+ * matrices, weights and the gate 16-byte aligned; eps >= 0 and finite.  rows == 0 -> FP8Q_OK. */
+typedef struct {
+  int64_t rows, cols;
+  int32_t h_dtype, w_dtype;    /* fp8q_dtype of h / h_out, and of w_pre / w_post / gate */
+  float alpha, eps;
+  const void* y;
+  int64_t ld_y;
+  const void* h;
+  int64_t ld_h;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+  void* h_out;
+  int64_t ld_h_out;
+  void* n_out;
+  int64_t ld_n;
+  uint8_t* q_row;
+  float* s_row;
+  int64_t ld_s_row;
+  float* rstd_post;
+  float* rstd_pre;
+} fp8q_norm_args;
+fp8q_status fp8q_norm_residual(const fp8q_norm_args* args, void* stream);
+
+/* Gradients of fp8q_norm_residual.  dn: BF16, the gradient of n; dh_out: that of h' from the
+ * residual path (h_dtype); y, w_*, gate and alpha as in the forward call; h: the stored h' (h_out),
+ * rstd_pre and (with w_post) rstd_post as the forward call saved them.  With xh = h rstd_pre,
+ * a = dn w_pre, yh = y rstd_post (y without w_post):
+ *   d = dh_out + rstd_pre (a - xh mean(a xh)),   dh = alpha d   (h_dtype; may be dh_out)
+ *   b = d gate w_post,  dy = rstd_post (b - yh mean(b yh))      (BF16; without w_post: d gate)
+ *   dw_pre = sum over rows of dn xh,  dgate = w_post * S,  dw_post = gate * S,  S = sum of d yh
+ * dh, dy and dw_pre are required; dw_post (needs w_post) and dgate (needs gate) are optional;
+ * these three are cols floats each, overwritten.  Row sums and column sums are FP32, added in an
+ * order that depends only on the sizes and the device, so results repeat exactly.
+ * workspace: device memory, 16-byte aligned, fp8q_norm_backward_workspace_bytes(rows, cols,
+ * h_dtype) bytes, used by the call's two kernels only.  The forward call's limits hold;
+ * rows == 0 writes zero sums. */
+typedef struct {
+  int64_t rows, cols;
+  int32_t h_dtype, w_dtype;
+  float alpha;
+  const void* dn;
+  int64_t ld_dn;
+  const void* dh_out;
+  int64_t ld_dh_out;
+  const void* y;
+  int64_t ld_y;
+  const void* h;
+  int64_t ld_h;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+  const float* rstd_post;
+  const float* rstd_pre;
+  void* dh;
+  int64_t ld_dh;
+  void* dy;
+  int64_t ld_dy;
+  float* dw_post;
+  float* dgate;
+  float* dw_pre;
+  void* workspace;
+  int64_t workspace_bytes;
+} fp8q_norm_backward_args;
+fp8q_status fp8q_norm_residual_backward(const fp8q_norm_backward_args* args, void* stream);
+
+/* Workspace bytes of fp8q_norm_residual_backward on the current device; 0 for sizes or a type
+ * that it refuses, and without a device. */
+size_t fp8q_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t h_dtype);
+
+/* [DSV3] "Mixed-precision framework" keeps gradients in FP32 (c_fp32_accumulate above); before
+ * the optimizer uses them a training step takes their global norm and clips:
+ *   norm = sqrt( sum over all items of grad^2 ),  coef = min(1, max_norm / (norm + eps)),
+ *   out = coef * grad, computed in FP32 and rounded once to the item's type.
+ * Each item is `numel` contiguous elements of `dtype` (fp8q_dtype) at any element-aligned
+ * address; out (same type) is where its clipped values go: grad itself (in place), or memory that
+ * overlaps no other item's grad or out (FP8Q_ERR_UNSUPPORTED otherwise; items may share a grad
+ * when none of them is clipped in place).  Items with numel == 0 are skipped.
+ * norm (device float, may be NULL) receives the norm before clipping (infinity where it passes
+ * FP32's range; the factor is formed in FP64); with no elements it is 0.
+ * Sums are formed in FP64 (finite gradients of any size give the correct norm) in an order that
+ * depends only on the sizes, alignments and the device, so results repeat exactly.  A norm of NaN
+ * makes every clipped value NaN; one of infinity makes the factor 0.  max_norm >= 0 (not NaN),
+ * eps >= 0 and finite.
+ * workspace: device memory, 16-byte aligned, of fp8q_clip_grad_workspace_bytes(n_items) bytes,
+ * used by the call's kernels only (not concurrently elsewhere).  Asynchronous on `stream`, one
+ * norm and one scaling launch per 1024 items. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int64_t dtype;               /* fp8q_dtype */
+} fp8q_grad_item;
+fp8q_status fp8q_clip_grad_norm(const fp8q_grad_item* items, int64_t n_items, double max_norm, double eps,
+                                float* norm, void* workspace, int64_t workspace_bytes, void* stream);
+size_t fp8q_clip_grad_workspace_bytes(int64_t n_items);
 
 /* Bytes of a scale-factor buffer: recipe MXFP8 (inner/32 scale columns) or NVFP4
  * (inner/16), `outer` rows, in `layout`.  Returns 0 for other recipes. */
