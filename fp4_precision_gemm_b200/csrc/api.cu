@@ -810,6 +810,17 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   if (st != FP8Q_OK) return st;
   p.status = d->base.load(std::memory_order_acquire);
 
+  const int few = grouped && !k_groups ? gemm_few_rows_tile(a->M, a->N, a->num_groups, d->num_sms) : 0;
+  if (few > 0) {
+    CUtensorMap mr, mw;
+    if (!make_map(&mr, a->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, kbytes, a->M, a->lda, 128, few,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&mw, a->b, CU_TENSOR_MAP_DATA_TYPE_UINT8, kbytes, (uint64_t)a->num_groups * a->N, a->ldb, 128, 128,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+      return FP8Q_ERR_CUDA;
+    return from_cuda(launch_gemm_few_rows(p, mr, mw, d->num_sms, s));
+  }
+
   CUtensorMap ma, mb, msb;
   const int64_t b_rows = grouped && !k_groups ? (int64_t)a->num_groups * a->N : a->N;
   const int64_t c_rows = k_groups ? (int64_t)a->num_groups * a->M : a->M;
@@ -831,16 +842,19 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
     msb = ma;
   }
   // the blockwise epilogues send their staged boxes by TMA: BF16 32 x 32 boxes (and the fused
-  // quantization's 32 x 64 code boxes) stored, FP32 boxes added
+  // quantization's 32 x 64 code boxes) stored, FP32 boxes added; grouped GEMMs' boxes are twice
+  // as wide (rows of 128 bytes)
+  const uint32_t wide = grouped ? 2 : 1;
+  const CUtensorMapSwizzle c_swizzle = grouped ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap mc = ma, mq = ma;
   if (a->recipe == FP8Q_BLOCKWISE && acc32 && a->M > 0 && a->N > 0) {
     // FP32 accumulation: 32 x 16 FP32 boxes added into C by TMA reduction
-    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a->N, c_rows, a->ldc * 4, 16, 32,
-                  CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a->N, c_rows, a->ldc * 4, 16 * wide, 32,
+                  c_swizzle))
       return FP8Q_ERR_CUDA;
   } else if (a->recipe == FP8Q_BLOCKWISE && a->M > 0 && a->N > 0) {
-    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->N, c_rows, a->ldc * 2, 32, 32,
-                  CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->N, c_rows, a->ldc * 2, 32 * wide, 32,
+                  c_swizzle))
       return FP8Q_ERR_CUDA;
     if (qout && !make_map(&mq, a->q_out, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->N, a->M, a->ld_q_out, 64, 32,
                           CU_TENSOR_MAP_SWIZZLE_64B))

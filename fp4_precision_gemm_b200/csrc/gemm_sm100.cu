@@ -517,8 +517,6 @@ namespace {
 
 constexpr int kBwPairM = 2 * kBM;               // 256 output rows per pair tile
 constexpr int kBwSb = 10;                       // scale ring: chunks of A/B scales staged ahead
-constexpr int kBwGo = 10;                       // MMA go barriers: a multiple of both the stage count
-                                                // and the two TMEM partial buffers
 
 // Pair tile shape: 256 x 256 outputs, 16 promotion warps.  wgrad (two FP32 operations per
 // element and chunk: the column scale, then the row scale) moves registers from the helper
@@ -548,11 +546,12 @@ struct BwCfg {
 // Shared memory of the blockwise kernel.  A scale-ring slot holds one chunk's scales:
 // wgrad: [B scales of the tile's 256 columns][A scales of the CTA's 128 rows];
 // fprop/dgrad: [A scales][the B scales of the tile's four 64-column groups].
-template <int L>
+template <int L, bool GROUPED>
 struct BwSmem {
   using C = BwCfg<L>;
   static constexpr bool wg = (L == kWgrad);
-  static constexpr int stages = 5;
+  static constexpr int stages = GROUPED ? 4 : 5;
+  static constexpr int go = 2 * stages;   // MMA go barriers: cycle with the stages and the two TMEM buffers
   static constexpr uint32_t slot_sbw = 0;
   static constexpr uint32_t slot_sa = wg ? C::BN * 4 : 0;
   static constexpr uint32_t slot_sb = slot_sa + kBM * 4;
@@ -560,14 +559,17 @@ struct BwSmem {
   static constexpr uint32_t a = 0;
   static constexpr uint32_t b = a + stages * kAStage;
   static constexpr uint32_t ring = b + stages * C::BStage;
-  // epilogue staging per promotion warp: 32 rows x epi_cols BF16 (wgrad: half the width)
-  static constexpr int epi_cols = 32;
+  // epilogue staging per promotion warp: 32 rows x epi_cols BF16 or half as many FP32.  Grouped
+  // GEMMs stage rows of 128 bytes, in the place of a fifth A/B stage: their K is short, so tiles
+  // end often, and the copy engine moves 128-byte rows in half the requests of 64-byte ones
+  // 32 experts, K 2048, N 7168, 65536 rows: 1314 -> 1263 us back to back; weight gradients of
+  // 32 x 2048 x 7168 into FP32: 1137 -> 1060 us; two or three buffers of 64-byte rows: no gain.
+  static constexpr int epi_cols = GROUPED ? 64 : 32;
   static constexpr uint32_t stage_c = 32 * epi_cols * 2;
-  // staging buffers 1024-byte aligned: the TMA store's 64-byte swizzle follows address bits
+  // staging buffers 1024-byte aligned: the TMA store's swizzle follows address bits
   static constexpr uint32_t cst = ((ring + kBwSb * slot_bytes + 1023) / 1024) * 1024;
   static constexpr uint32_t bars = cst + C::EpiWarps * stage_c;
-  static constexpr uint32_t n_bars = kBwGo + stages + 2 * kBwSb + 1 + C::EpiWarps / 2;
-  static_assert(kBwGo % stages == 0 && kBwGo % 2 == 0, "go slots must cycle with the stages and TMEM buffers");
+  static constexpr uint32_t n_bars = go + stages + 2 * kBwSb + 1 + C::EpiWarps / 2;
   static constexpr uint32_t misc = bars + n_bars * 8;
   static constexpr uint32_t groups = misc + 16;
   // fused output quantization: each promotion warp's 32 row amaxes, read by its partner warp
@@ -598,8 +600,12 @@ __device__ __forceinline__ Tile pair_tile_of(int t, const GemmParams& p, int row
   raster_pos(t, p, row_tiles, rt, nt);
   T.n0 = nt * BN;
   if (p.num_groups > 0) {
-    int g = 0;
-    while (g + 1 < p.num_groups && prefix[g + 1] <= rt) ++g;
+    int g = 0, past = p.num_groups;   // the last expert with prefix[g] <= rt
+    while (past - g > 1) {
+      const int mid = (g + past) >> 1;
+      if (prefix[mid] <= rt) g = mid;
+      else past = mid;
+    }
     T.g = g;
     T.m0 = offs[g] + (rt - prefix[g]) * kBwPairM;
     end = offs[g + 1];
@@ -686,7 +692,8 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
     gemm_blockwise_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap tma_a,
                           const __grid_constant__ CUtensorMap tma_b, const __grid_constant__ CUtensorMap tma_sb,
                           const __grid_constant__ CUtensorMap tma_c, const __grid_constant__ CUtensorMap tma_q) {
-  using S = BwSmem<L>;
+  using S = BwSmem<L, GROUPED>;
+  constexpr int kBwGo = S::go;
   constexpr bool kWg = (L == kWgrad);
   constexpr bool ACC32 = EPI == kEpiAcc32, QOUT = EPI == kEpiQuant;
   // BF16 output or FP32 accumulation, not grouped: the last wave may be split into K ranges,
@@ -1173,7 +1180,7 @@ static cudaError_t blockwise_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute
     }();
     if (regs != C::RegsLaunch) return cudaErrorInvalidConfiguration;
   }
-  const int smem = (int)BwSmem<L>::alloc;
+  const int smem = (int)BwSmem<L, G>::alloc;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cfg = cudaLaunchConfig_t{};

@@ -184,6 +184,12 @@ cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& tma_a, const CUt
                         const CUtensorMap& tma_sb, const CUtensorMap& tma_c, const CUtensorMap& tma_q,
                         const CUtensorMap& tma_ws, int num_sms, cudaStream_t s);
 
+// Grouped fprop / dgrad with few rows per expert: its own kernel (gemm_rows.cu), with TMA boxes
+// of this many rows of A (0: the large kernel) and 128 rows of B.  Defined in gemm_rows.cu.
+int gemm_few_rows_tile(int64_t M, int64_t N, int groups, int num_sms);
+cudaError_t launch_gemm_few_rows(const GemmParams& p, const CUtensorMap& tma_a, const CUtensorMap& tma_w, int num_sms,
+                                 cudaStream_t s);
+
 // Workspace bytes that a blockwise BF16 GEMM with these parameters uses to split its last,
 // partial wave into K ranges on the current device (0: it would not split).
 size_t blockwise_workspace_bytes(const GemmParams& p, int num_sms);

@@ -124,6 +124,27 @@ def test_rows_padded_strides_and_stream(cuda_lib, layout):
     assert bool((wide[:, N:] == 7.0).all())
 
 
+@pytest.mark.parametrize("layout", ["fprop", "dgrad"])
+@pytest.mark.parametrize("counts", [[1], [0, 7, 0, 33, 64, 1], [512], [3] * 100, [100, 0, 412]], ids=str)
+def test_few_rows_equal_many_rows_to_the_bit(cuda_lib, layout, counts):
+    """The same rows alone, and in front of another expert's thousand rows: whatever kernel a size
+    selects, a row's result is the same sum in the same order."""
+    fq = cuda_lib
+    G, M, K, N, extra = len(counts), sum(counts), 640, 392, 1000
+    dgrad = layout == "dgrad"
+    a, b = codes((M + extra, K), 71), codes((G + 1, N, K), 72)
+    sa, sb = scales((K // 128, M + extra), 73), scales((G + 1, 5, 4) if dgrad else (G + 1, 4, 5), 74)
+    lay = fq.FP8Q_DGRAD if dgrad else fq.FP8Q_FPROP
+    acc = torch.randn((M + extra, N), device="cuda")
+    few, many = acc[:M].clone(), acc.clone()
+    for out in (None, 1):
+        one = fq.gemm(a[:M], b[:G], layout=lay, a_scale=sa, b_scale=sb[:G], m_offsets=offsets(counts),
+                      out=few if out else None, accumulate_fp32=bool(out))
+        all_ = fq.gemm(a, b, layout=lay, a_scale=sa, b_scale=sb, m_offsets=offsets(counts + [extra]),
+                       out=many if out else None, accumulate_fp32=bool(out))
+        assert torch.equal(one, all_[:M])
+
+
 def wgrad_reference(x, sx, y, sy, counts):
     c, t, at = [], [], 0
     for n in counts:
