@@ -10,6 +10,7 @@ Two layers, same names as the C ABI:
   * ``quantize_1x128(x, ...)``, ``quantize_128x128``, ``quantize_mx32``, ``quantize_tensor``,
     ``rht16_quantize_sr``, ``gemm`` take torch tensors, allocate the outputs and call them.
 """
+import array
 import contextlib
 import ctypes
 import os
@@ -205,15 +206,21 @@ def _check(st, where):
 
 def _stream(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        # the handle alone: building a torch.cuda.Stream costs several microseconds a call
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(device, stream):
     """Makes `device` current for a call on its tensors (and refuses a stream of another device)."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _ptr(t):
@@ -297,7 +304,7 @@ def fp8q_norm_backward_workspace_bytes(rows, cols, h_dtype):
 
 
 def fp8q_clip_grad_norm(items, n_items, max_norm, eps, norm, workspace, workspace_bytes, stream):
-    """items: a ctypes array of GradItem (or None with n_items == 0)."""
+    """items: a ctypes array of GradItem or its address (or None with n_items == 0)."""
     return lib().fp8q_clip_grad_norm(items, n_items, max_norm, eps, norm, workspace, workspace_bytes, stream)
 
 
@@ -658,17 +665,23 @@ def _norm_operands(y, h, w_pre, w_post, gate, like_y=(), like_h=(), rows=()):
     R, C = y.shape
     if h.dtype not in _DTYPES or w_pre.dtype not in _DTYPES:
         raise ValueError("h and the weights must be bfloat16 or float32")
+    index, shape, hd, wd = y.get_device(), y.shape, h.dtype, w_pre.dtype
     for t in (h, *like_y, *like_h):
-        if t.shape != y.shape or t.device != y.device or (C > 1 and t.stride(1) != 1):
+        if t.shape != shape or t.get_device() != index or t.stride(1) != 1:
             raise ValueError("matrices must be row-major, of y's shape and on its device")
-    if any(t.dtype != torch.bfloat16 for t in like_y) or any(t.dtype != h.dtype for t in like_h):
-        raise ValueError("matrices of y's kind must be bfloat16, those of h's kind of h's type")
+    for t in like_y:
+        if t.dtype != torch.bfloat16:
+            raise ValueError("matrices of y's kind must be bfloat16")
+    for t in like_h:
+        if t.dtype != hd:
+            raise ValueError("matrices of h's kind must be of h's type")
     for t in (w_pre, w_post, gate):
-        if t is not None and (t.dtype != w_pre.dtype or t.device != y.device or tuple(t.shape) != (C,)
+        if t is not None and (t.dtype != wd or t.get_device() != index or t.dim() != 1 or t.numel() != C
                               or not t.is_contiguous()):
             raise ValueError("w_pre, w_post and gate must be contiguous vectors of y's columns, of one type")
     for t in rows:
-        if t.dtype != torch.float32 or t.device != y.device or tuple(t.shape) != (R,) or not t.is_contiguous():
+        if (t.dtype != torch.float32 or t.get_device() != index or t.dim() != 1 or t.numel() != R
+                or not t.is_contiguous()):
             raise ValueError("rstd vectors must be contiguous float32, one value per row")
     return _DTYPES[h.dtype], _DTYPES[w_pre.dtype]
 
@@ -754,24 +767,28 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
         raise ValueError("no gradients")
     if len(outs) != len(grads):
         raise ValueError("out must have one tensor per gradient")
-    dev = grads[0].device
-    flat = []
-    for g, o in zip(grads, outs):
-        dt = _DTYPES.get(g.dtype)
-        if dt is None or g.device != dev or not g.is_cuda or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
-        n = g.numel()
-        if o is not g and (o.dtype != g.dtype or o.device != dev or o.numel() != n or not o.is_contiguous()):
-            raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
-        flat += (g.data_ptr(), o.data_ptr(), n, dt)
-    items = (ctypes.c_int64 * len(flat))(*flat)        # GradItem is four 64-bit words
+    # whole lists at a time: hundreds of tensors are usual, and a loop of checks costs microseconds each
+    dev, index, n = grads[0].device, grads[0].get_device(), len(grads)
+    types, sizes = [_DTYPES.get(g.dtype) for g in grads], [g.numel() for g in grads]
+    if (index < 0 or None in types or [g.get_device() for g in grads].count(index) != n
+            or False in [g.is_contiguous() for g in grads]):
+        raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
+    if out is not None and ([_DTYPES.get(o.dtype) for o in outs] != types or [o.numel() for o in outs] != sizes
+                            or [o.get_device() for o in outs].count(index) != n
+                            or False in [o.is_contiguous() for o in outs]):
+        raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
+    words = [0] * (4 * n)                                  # GradItem is four 64-bit words
+    words[0::4] = [g.data_ptr() for g in grads]
+    words[1::4] = words[0::4] if out is None else [o.data_ptr() for o in outs]
+    words[2::4], words[3::4] = sizes, types
+    items = array.array("q", words)
     nbytes = fp8q_clip_grad_workspace_bytes(len(grads))
     ws = torch.empty(nbytes + 16, dtype=torch.uint8, device=dev)     # the norm after the partial sums
     norm = ws[nbytes:nbytes + 4].view(torch.float32)[0]
     if stream is not None:
         ws.record_stream(stream)
     with _on(dev, stream):
-        st = fp8q_clip_grad_norm(items, len(grads), max_norm, eps, _ptr(norm), _ptr(ws), nbytes, _stream(stream))
+        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps, _ptr(norm), _ptr(ws), nbytes, _stream(stream))
     _check(st, "fp8q_clip_grad_norm")
     return norm
 

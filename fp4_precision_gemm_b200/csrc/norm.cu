@@ -58,22 +58,74 @@ __device__ __forceinline__ void put8(uint8_t* row, int col, const float (&x)[8])
   }
 }
 
-// Sum over the CTA in a fixed order (lanes, then warps), the same in every thread.  `sh` must
-// not be the buffer of the previous sum; `ok` becomes whether every thread's was set.
+// Sum over the CTA in a fixed order (lanes, then warps), the same in every thread.  `sh` (zero
+// where there is no warp) must not be the buffer of the previous sum; `ok` becomes whether
+// every thread's was set.
 __device__ __forceinline__ float row_sum(float v, float* sh, int& ok) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   ok = __syncthreads_and(ok);
-  v = sh[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) v += sh[w];
-  return v;
+  const float4* q = reinterpret_cast<const float4*>(sh);
+  const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+  return (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) +
+         (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
 }
 
 struct NormShared {
+  alignas(16) float sums[2][kMaxWarps];
   uint64_t full[2 * kMaxStages];
-  float sums[2][kMaxWarps];
   int abort_flag;
+};
+
+// The thread's columns of the weights, in FP32: w_pre, and gate * w_post (1 for the missing
+// ones).  Kept in registers over all rows where they fit (KEEP), else read again for every row.
+template <int NV, bool W32, bool KEEP>
+struct Weights {
+  float pre[KEEP ? NV : 1][8], mid[KEEP ? NV : 1][8];
+
+  static __device__ __forceinline__ void load_pre(const NormParams& p, int col, float (&w)[8]) {
+    get8<W32>(static_cast<const uint8_t*>(p.w_pre), col, w);
+  }
+  static __device__ __forceinline__ void load_mid(const NormParams& p, int col, float (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = 1.0f;
+    if (p.w_post != nullptr) get8<W32>(static_cast<const uint8_t*>(p.w_post), col, w);
+    if (p.gate != nullptr) {
+      float g[8];
+      get8<W32>(static_cast<const uint8_t*>(p.gate), col, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] *= g[k];
+    }
+  }
+  __device__ __forceinline__ void init(const NormParams& p, int tid, int T) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int col = (v * T + tid) * 8;
+        if (col < p.cols) {
+          load_pre(p, col, pre[v]);
+          load_mid(p, col, mid[v]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get_pre(const NormParams& p, int v, int col, float (&w)[8]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = pre[v][k];
+    } else {
+      load_pre(p, col, w);
+    }
+  }
+  __device__ __forceinline__ void get_mid(const NormParams& p, int v, int col, float (&w)[8]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = mid[v][k];
+    } else {
+      load_mid(p, col, w);
+    }
+  }
 };
 
 __device__ __forceinline__ float rms_factor(float sum, int cols, float eps) {
@@ -89,9 +141,8 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
   __shared__ NormShared sh;
   const int tid = threadIdx.x, T = blockDim.x, C = p.cols;
   const uint32_t ybytes = (uint32_t)C * 2, hbytes = (uint32_t)C * (H32 ? 4 : 2), stage = ybytes + hbytes;
-  const uint8_t* w_post = static_cast<const uint8_t*>(p.w_post);
-  const uint8_t* gate = static_cast<const uint8_t*>(p.gate);
-  const uint8_t* w_pre = static_cast<const uint8_t*>(p.w_pre);
+  const bool post = p.w_post != nullptr;
+  if (tid < 2 * kMaxWarps) sh.sums[0][tid] = 0.0f;
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1);
     sh.abort_flag = 0;
@@ -112,6 +163,8 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
       if (row >= p.rows) break;
       load(row, issued);
     }
+  Weights<NV, W32, true> W;
+  W.init(p, tid, T);
   uint32_t it = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += step, ++it) {
     const int s = it % p.stages;
@@ -119,7 +172,7 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
     const uint8_t* ys = ring + s * stage;
     const uint8_t* hs = ys + ybytes;
     float rq = 1.0f;
-    if (w_post != nullptr) {
+    if (post) {
       float ss = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -140,27 +193,18 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[v][k] = 0.0f;
       if (col < C) {
-        float y[8], h[8], w[8], g[8];
+        float y[8], h[8], w[8];
         get8<false>(ys, col, y);
         get8<H32>(hs, col, h);
-        if (w_post != nullptr) {
-          get8<W32>(w_post, col, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] *= rq * w[k];
-        }
-        if (gate != nullptr) {
-          get8<W32>(gate, col, g);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] *= g[k];
-        }
+        W.get_mid(p, v, col, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          x[v][k] = fmaf(p.alpha, h[k], y[k]);
+          x[v][k] = fmaf(p.alpha, h[k], y[k] * rq * w[k]);
           ss = fmaf(x[v][k], x[v][k], ss);
         }
       }
     }
-    const float rp = rms_factor(row_sum(ss, sh.sums[w_post != nullptr ? 1 : it & 1], ok), C, p.eps);
+    const float rp = rms_factor(row_sum(ss, sh.sums[post ? 1 : it & 1], ok), C, p.eps);
     if (!ok) break;
     // every thread has read the stage
     if (tid == 0 && row + p.stages * step < p.rows) {
@@ -176,7 +220,7 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
       if (in) {
         float w[8];
         put8<H32>(hout, col, x[v]);
-        get8<W32>(w_pre, col, w);
+        W.get_pre(p, v, col, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) n[k] = x[v][k] * rp * w[k];
         if (p.n_out != nullptr) put8<false>(static_cast<uint8_t*>(p.n_out) + row * p.ld_n * 2, col, n);
@@ -201,7 +245,7 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
     }
     if (tid == 0) {
       if (p.rstd_pre != nullptr) p.rstd_pre[row] = rp;
-      if (w_post != nullptr && p.rstd_post != nullptr) p.rstd_post[row] = rq;
+      if (post && p.rstd_post != nullptr) p.rstd_post[row] = rq;
     }
   }
   if (tid == 0) {
@@ -222,11 +266,10 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
   const int tid = threadIdx.x, T = blockDim.x, C = p.cols, S = p.stages;
   constexpr int HB = H32 ? 4 : 2;
   const uint32_t nbytes = (uint32_t)C * 2, hbytes = (uint32_t)C * HB, stage = 2 * nbytes + 2 * hbytes;
-  const uint8_t* w_post = static_cast<const uint8_t*>(p.w_post);
-  const uint8_t* gate = static_cast<const uint8_t*>(p.gate);
-  const uint8_t* w_pre = static_cast<const uint8_t*>(p.w_pre);
+  const bool post = p.w_post != nullptr;
   uint64_t* full_a = sh.full;
   uint64_t* full_y = sh.full + kMaxStages;
+  if (tid < 2 * kMaxWarps) sh.sums[0][tid] = 0.0f;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_a[s], 1);
@@ -265,6 +308,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc_pre[v][k] = acc_s[v][k] = 0.0f;
+  Weights<NV, W32, (NV <= 2)> W;
+  W.init(p, tid, T);
   const float inv_c = 1.0f / (float)C;
   int64_t j = 0;
   int ok = 1;
@@ -277,7 +322,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
     const uint8_t* hs = dns + nbytes;
     const uint8_t* dhs = hs + hbytes;
     const uint8_t* ys = dhs + hbytes;
-    const float rp = p.rstd_pre[row], rq = w_post != nullptr ? p.rstd_post[row] : 1.0f;
+    const float rp = p.rstd_pre[row], rq = post ? p.rstd_post[row] : 1.0f;
     float c1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -286,7 +331,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         float dn[8], h[8], w[8];
         get8<false>(dns, col, dn);
         get8<H32>(hs, col, h);
-        get8<W32>(w_pre, col, w);
+        W.get_pre(p, v, col, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float t = dn[k] * (h[k] * rp);
@@ -295,11 +340,11 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         }
       }
     }
-    c1 = row_sum(c1, sh.sums[w_post != nullptr ? 0 : j & 1], ok) * inv_c;
+    c1 = row_sum(c1, sh.sums[post ? 0 : j & 1], ok) * inv_c;
     if (!ok) break;
     // every thread has left row j - 1: its stage's remaining parts may be refilled
     if (tid == 0 && j > 0) {
-      if (w_post == nullptr) load_a(j - 1 + S);
+      if (!post) load_a(j - 1 + S);
       load_y(j - 1 + S);
     }
     float d[NV][8], c2 = 0.0f;
@@ -315,7 +360,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         get8<false>(dns, col, dn);
         get8<H32>(hs, col, h);
         get8<H32>(dhs, col, g);
-        get8<W32>(w_pre, col, w);
+        W.get_pre(p, v, col, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           d[v][k] = fmaf(rp, dn[k] * w[k] - h[k] * rp * c1, g[k]);
@@ -326,24 +371,16 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         get8<false>(ys, col, y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc_s[v][k] = fmaf(d[v][k], y[k] * rq, acc_s[v][k]);
-        if (gate != nullptr) {
-          get8<W32>(gate, col, w);
+        W.get_mid(p, v, col, w);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) d[v][k] *= w[k];
+        for (int k = 0; k < 8; ++k) {
+          d[v][k] *= w[k];
+          c2 = fmaf(d[v][k], y[k] * rq, c2);
         }
-        if (w_post != nullptr) {
-          get8<W32>(w_post, col, w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            d[v][k] *= w[k];
-            c2 = fmaf(d[v][k], y[k] * rq, c2);
-          }
-        } else {
-          put8<false>(dy, col, d[v]);
-        }
+        if (!post) put8<false>(dy, col, d[v]);
       }
     }
-    if (w_post != nullptr) {
+    if (post) {
       c2 = row_sum(c2, sh.sums[1], ok) * inv_c;
       if (tid == 0) load_a(j + S);   // dn, h', dh' of row j have been read by every thread
 #pragma unroll
@@ -364,7 +401,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
       atomicExch(p.status, kDevTimeout);
       for (int64_t i = j; i < j + S && i < mine; ++i) {
         const uint32_t ph = (uint32_t)(i / S) & 1;
-        if (i < j + S - (w_post == nullptr && j > 0)) mbar_wait_drain(&full_a[i % S], ph, kNormWaitNs);
+        if (i < j + S - (!post && j > 0)) mbar_wait_drain(&full_a[i % S], ph, kNormWaitNs);
         if (i < j + S - (j > 0)) mbar_wait_drain(&full_y[i % S], ph, kNormWaitNs);
       }
     }
@@ -418,21 +455,24 @@ struct NormShape {
   int nv, threads, stages, smem, grid;
 };
 
-// Threads own up to 4 groups of 8 columns (512 threads at most).  Up to 4 rows are staged, as
-// many as shared memory takes; narrow rows share an SM between several CTAs.
-NormShape norm_shape(int64_t rows, int cols, int row_bytes, int num_sms) {
+// Threads own nv groups of 8 columns (512 threads at most).  With a row or two per SM the most
+// threads per row are the fastest; with many rows wide threads let an SM hold several CTAs,
+// whose row sums and barriers hide behind one another (`wide`, the forward kernel).  Up to 4 rows
+// are staged per CTA, as many as its share of shared memory takes.
+NormShape norm_shape(int64_t rows, int cols, int row_bytes, int num_sms, bool wide) {
   constexpr int kSmem = 220 * 1024;
   NormShape s;
   const int vecs = (cols + 7) / 8;
   s.nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+  if (wide && rows > 2 * num_sms) s.nv = 4;
   s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
-  s.stages = kSmem / row_bytes;
+  int ctas = 512 / s.threads;
+  if (ctas > kSmem / (row_bytes + 1024)) ctas = kSmem / (row_bytes + 1024);
+  if (ctas < 1) ctas = 1;
+  s.stages = (kSmem / ctas - 1024) / row_bytes;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   if (s.stages < 1) s.stages = 1;
   s.smem = s.stages * row_bytes;
-  int ctas = kSmem / (s.smem + 1024);
-  if (ctas > 512 / s.threads) ctas = 512 / s.threads;
-  if (ctas < 1) ctas = 1;
   const int64_t g = (int64_t)ctas * num_sms;
   s.grid = (int)(rows < g ? rows : g);
   return s;
@@ -449,7 +489,7 @@ cudaError_t launch_rows(K kern, const NormShape& s, const NormParams& p, cudaStr
 }  // namespace
 
 int norm_backward_ctas(int64_t rows, int cols, bool h32, int num_sms) {
-  return norm_shape(rows, cols, cols * (h32 ? 12 : 8), num_sms).grid;
+  return norm_shape(rows, cols, cols * (h32 ? 12 : 8), num_sms, false).grid;
 }
 
 #define FP8Q_NORM(KERNEL, N, H, W) \
@@ -461,7 +501,7 @@ int norm_backward_ctas(int64_t rows, int cols, bool h32, int num_sms) {
   FP8Q_NORM(KERNEL, 4, false, true) FP8Q_NORM(KERNEL, 4, true, false) FP8Q_NORM(KERNEL, 4, true, true)
 
 cudaError_t launch_norm_forward(const NormParams& p, bool h32, bool w32, int num_sms, cudaStream_t st) {
-  const NormShape s = norm_shape(p.rows, p.cols, p.cols * (h32 ? 6 : 4), num_sms);
+  const NormShape s = norm_shape(p.rows, p.cols, p.cols * (h32 ? 6 : 4), num_sms, true);
   NormParams q = p;
   q.stages = s.stages;
   FP8Q_NORMS(norm_forward_kernel)
@@ -480,7 +520,7 @@ static cudaError_t launch_norm_backward_rows(const NormParams& p, bool h32, bool
 cudaError_t launch_norm_backward(const NormParams& p, bool h32, bool w32, int num_sms, cudaStream_t st) {
   int ctas = 0;
   if (p.rows > 0) {
-    const NormShape s = norm_shape(p.rows, p.cols, p.cols * (h32 ? 12 : 8), num_sms);
+    const NormShape s = norm_shape(p.rows, p.cols, p.cols * (h32 ? 12 : 8), num_sms, false);
     const cudaError_t e = launch_norm_backward_rows(p, h32, w32, s, st);
     if (e != cudaSuccess) return e;
     ctas = s.grid;
