@@ -3,10 +3,11 @@
 //   out = coef * g (rounded once).
 //
 // Bound by bytes: every gradient is read for the norm, read again for the scaling and written.
-// The tensors are cut into 16 KB chunks whose starts are 16-byte aligned in memory; persistent
-// CTAs walk the chunks of all tensors as one list, so a launch's ramp and tail are paid once
-// and small tensors share a wave.  The scaling pass walks the list from its end: the chunks that
-// the norm pass read last are still in L2.
+// The tensors are cut into 16 KB chunks whose starts are 16-byte aligned in memory; the chunks of
+// all tensors are one list over which persistent CTAs stride, so a launch's ramp and tail are paid
+// once and small tensors share a wave.  The next chunk's loads are in flight under the current
+// one's arithmetic.  The scaling pass walks the list from its end: what the norm pass read last is
+// still in L2; its stores are marked as not to be kept there.
 //
 // Two launches, no atomics: each CTA of the norm pass writes one FP64 partial, and every CTA of
 // the scaling pass adds all partials in the same order, so results do not change from run to run.
@@ -27,6 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;                                    // 16-byte vectors per thread and chunk
 constexpr int kChunkBytes = kThreads * kVecs * 16;
+constexpr int kLine = 128;                                  // chunks start at whole cache lines
 
 // One chunk: vectors at 16-byte aligned addresses covering elements [e0, e0 + chunk) of tensor i;
 // elements outside [0, numel) belong to nobody (the tensor's unaligned head and its tail).
@@ -36,20 +38,29 @@ struct Chunk {
   const uint8_t* g;   // address of element e0 (16-byte aligned)
 };
 
+// The tensor of chunk c.
 template <int MAX>
-__device__ __forceinline__ Chunk chunk_of(const ClipTensors<MAX>& P, int c) {
+__device__ __forceinline__ int tensor_of(const ClipTensors<MAX>& P, int c) {
   int lo = 0, hi = P.n;                 // chunk_begin[lo] <= c < chunk_begin[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (P.chunk_begin[mid] <= c) lo = mid;
     else hi = mid;
   }
+  return lo;
+}
+
+// Chunk c, its tensor found from `lo`, that of the CTA's chunk before it.
+template <int MAX>
+__device__ __forceinline__ Chunk chunk_of(const ClipTensors<MAX>& P, int c, int& lo) {
+  while (P.chunk_begin[lo + 1] <= c) ++lo;
+  while (P.chunk_begin[lo] > c) --lo;
   Chunk C;
   C.i = lo;
   C.esize = P.numel[lo] < 0 ? 4 : 2;
   C.n = P.numel[lo] < 0 ? -P.numel[lo] : P.numel[lo];
   const uint8_t* base = static_cast<const uint8_t*>(P.grad[lo]);
-  const int64_t head = (int64_t)(reinterpret_cast<uintptr_t>(base) & 15);
+  const int64_t head = (int64_t)(reinterpret_cast<uintptr_t>(base) & (kLine - 1));
   const int64_t off = (int64_t)(c - P.chunk_begin[lo]) * kChunkBytes - head;   // bytes from element 0
   C.e0 = off / C.esize;                 // exact: the head is a whole number of elements
   C.g = base + off;
@@ -124,12 +135,23 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
                                                              double* partials) {
   __shared__ double sh[kThreads / 32];
   double acc = 0.0;
-  for (int c = blockIdx.x; c < P.chunk_begin[P.n]; c += gridDim.x) {
-    const Chunk C = chunk_of(P, c);
-    uint4 v[kVecs];
+  const int end = P.chunk_begin[P.n];
+  int c = blockIdx.x, i = c < end ? tensor_of(P, c) : 0, esize = 4;
+  uint4 next[kVecs];
+  auto fetch = [&](int at) {
+    const Chunk C = chunk_of(P, at, i);
+    esize = C.esize;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) v[k] = load_vec(C, k * kThreads + threadIdx.x);
-    if (C.esize == 4) {
+    for (int k = 0; k < kVecs; ++k) next[k] = load_vec(C, k * kThreads + threadIdx.x);
+  };
+  if (c < end) fetch(c);
+  for (; c < end; c += gridDim.x) {
+    uint4 v[kVecs];
+    const int es = esize;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) v[k] = next[k];
+    if (c + (int)gridDim.x < end) fetch(c + gridDim.x);   // in flight under this chunk's squares
+    if (es == 4) {
 #pragma unroll
       for (int k = 0; k < kVecs; k += 2) {
         const float x[8] = {__uint_as_float(v[k].x), __uint_as_float(v[k].y), __uint_as_float(v[k].z),
@@ -163,13 +185,24 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
   const float coef = ratio >= 1.0 ? 1.0f : (float)ratio;   // a NaN norm gives a NaN factor
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   if (in_place && coef == 1.0f) return;                    // 1 * g is g: nothing to write
-  const int total = P.chunk_begin[P.n];
-  for (int b = blockIdx.x; b < total; b += gridDim.x) {
-    const Chunk C = chunk_of(P, total - 1 - b);
+  int c = P.chunk_begin[P.n] - 1 - (int)blockIdx.x;
+  if (c < 0) return;
+  int i = tensor_of(P, c);
+  uint4 next[kVecs];
+  Chunk N;
+  auto fetch = [&](int at) {
+    N = chunk_of(P, at, i);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) next[k] = load_vec(N, k * kThreads + threadIdx.x);
+  };
+  fetch(c);
+  for (; c >= 0; c -= gridDim.x) {
+    const Chunk C = N;
     const int per = 16 / C.esize;
     uint4 v[kVecs];
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) v[k] = load_vec(C, k * kThreads + threadIdx.x);
+    for (int k = 0; k < kVecs; ++k) v[k] = next[k];
+    if (c >= (int)gridDim.x) fetch(c - gridDim.x);
     uint8_t* out = static_cast<uint8_t*>(P.out[C.i]) + C.e0 * C.esize;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
 #pragma unroll
@@ -186,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
       const int64_t e = C.e0 + (int64_t)vec * per;
       uint8_t* q = out + (int64_t)vec * 16;
       if (aligned && e >= 0 && e + per <= C.n) {
-        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        __stcs(reinterpret_cast<uint4*>(q), make_uint4(w[0], w[1], w[2], w[3]));
       } else if (e + per > 0 && e < C.n) {
         if (C.esize == 4) {
 #pragma unroll
@@ -203,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
 }
 
 int clip_chunks(const void* grad, int64_t bytes) {
-  return bytes == 0 ? 0 : (int)(((int64_t)(reinterpret_cast<uintptr_t>(grad) & 15) + bytes + kChunkBytes - 1) / kChunkBytes);
+  return bytes == 0 ? 0 : (int)(((int64_t)(reinterpret_cast<uintptr_t>(grad) & (kLine - 1)) + bytes + kChunkBytes - 1) / kChunkBytes);
 }
 
 template <int MAX>
