@@ -56,28 +56,18 @@ struct TileSmem {
 template <bool ROW, bool COL>
 constexpr int kTileQuantCtas = (ROW && !COL) ? 3 : 4;
 
-// Rows of one 128-row band: source rows [r0, rend) of x, and their place in the transposed
-// output, columns [d0, d0 + 128) of rows d_ld long.
+// Rows of one 128-row band of a grouped (ragged) call: source rows [r0, rend) of x, and their
+// place in the transposed output, columns [d0, d0 + 128) of rows d_ld long; c0: first column.
 struct Band {
-  int64_t r0, rend, d0, d_ld;
+  int64_t r0, rend, d0, d_ld, c0;
 };
 
 // One 128x128 tile (index `tile` of the call, grouped calls counting every matrix's tiles)
-// quantized by the CTA's 256 threads.
-template <int MODE, bool ROW, bool COL>
-__device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_t tile, const Band& B, int64_t c0,
-                                                TileSmem& sm);
-
-template <int MODE, bool ROW, bool COL>
-__device__ __forceinline__ void tile_quant_tile(const TileQuantParams& P, int64_t tile, TileSmem& sm) {
-  const int64_t t = P.batch_tiles ? tile % P.batch_tiles : tile;   // within its matrix
-  const int64_t r0 = (t / P.tiles_c) * 128;
-  tile_quant_band<MODE, ROW, COL>(P, tile, Band{r0, P.rows, r0, P.rows}, (t % P.tiles_c) * 128, sm);
-}
-
-template <int MODE, bool ROW, bool COL>
-__device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_t tile, const Band& B, int64_t c0,
-                                                TileSmem& sm) {
+// quantized by the CTA's 256 threads.  RAGGED: the tile of `B` instead; many of those bands end
+// before their 128th row, and a warp without rows only stores zeros.
+template <int MODE, bool ROW, bool COL, bool RAGGED = false>
+__device__ __forceinline__ void tile_quant_tile(const TileQuantParams& P, int64_t tile, TileSmem& sm,
+                                                const Band B = Band()) {
   auto& red = sm.red;
   auto& colsf = sm.colsf;
   auto& colexp = sm.colexp;
@@ -87,12 +77,15 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
   const int cs = t & 15, rb = t >> 4;
   // grouped calls: CTA -> (matrix b, tile within it); every operand pointer moves by b strides
   const int64_t bidx = P.batch_tiles ? tile / P.batch_tiles : 0;
+  tile -= bidx * P.batch_tiles;
   const uint16_t* X = P.x + bidx * P.x_bstride;
   uint8_t* QR = P.q_row ? P.q_row + bidx * P.q_row_bstride : nullptr;
   uint8_t* QC = P.q_col ? P.q_col + bidx * P.q_col_bstride : nullptr;
   uint8_t* SR = P.s_row ? (uint8_t*)P.s_row + bidx * P.s_row_bstride : nullptr;
   uint8_t* SC = P.s_col ? (uint8_t*)P.s_col + bidx * P.s_col_bstride : nullptr;
-  const int64_t r0 = B.r0;
+  const int64_t r0 = RAGGED ? B.r0 : (tile / P.tiles_c) * 128;
+  const int64_t c0 = RAGGED ? B.c0 : (tile % P.tiles_c) * 128;
+  const int64_t rend = RAGGED ? B.rend : P.rows;
   const int64_t col = c0 + cs * 8;
   const bool cok = col < P.cols;
 
@@ -100,7 +93,7 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t row = r0 + rb * 8 + p;
-    v[p] = (cok && row < B.rend) ? ldg_nc_v4(X + row * P.ld_x + col) : make_uint4(0, 0, 0, 0);
+    v[p] = (cok && row < rend) ? ldg_nc_v4(X + row * P.ld_x + col) : make_uint4(0, 0, 0, 0);
   }
 
   // ---------------------------------------------------------------- amax reductions
@@ -154,7 +147,7 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
         const int cc = (wd >> 2) * 8 + (wd & 3) * 2 + h;
         const float sf = e4m3_sf(bf16_bits_to_float(h ? (m >> 16) : (m & 0xFFFFu)));
         colsf[cc] = sf;
-        if (c0 + cc < P.cols) ((float*)SC)[(B.d0 >> 7) * P.ld_s_col + c0 + cc] = __frcp_rn(sf);
+        if (c0 + cc < P.cols) ((float*)SC)[((RAGGED ? B.d0 : r0) >> 7) * P.ld_s_col + c0 + cc] = __frcp_rn(sf);
       }
       __syncthreads();
     } else {  // MX: 32-row block b = warp / 2 spans warps 2b and 2b+1
@@ -188,7 +181,8 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
   }
 
   // ---------------------------------------------------------------- rowwise output
-  if (ROW) {
+  const bool has_rows = !RAGGED || r0 + warp * 16 < rend;   // warp-uniform
+  if (ROW && has_rows) {
     // 1x128: the 16 lanes of a row group hold the same 8 row maxima; lane cs divides for row
     // cs % 8 and the scales are shuffled out (one IEEE division per thread instead of 8)
     float sf_own = 1.0f;
@@ -199,7 +193,7 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
       // lane cs < 8 of the row group also writes row cs's decode scale (one reciprocal per
       // lane instead of one per row with a single lane active)
       const int64_t row = r0 + rb * 8 + cs;
-      if (cs < 8 && row < B.rend) ((float*)SR)[(c0 >> 7) * P.ld_s_row + row] = __frcp_rn(sf_own);
+      if (cs < 8 && row < rend) ((float*)SR)[(c0 >> 7) * P.ld_s_row + row] = __frcp_rn(sf_own);
     }
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
@@ -215,7 +209,7 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
         e = mx_exponent(bf16_bits_to_float(abits));
         sf = pow2_neg(e);
       }
-      if (row < B.rend && cok) {
+      if (row < rend && cok) {
         const float2 s2 = make_float2(sf, sf);
         uint32_t c[4];
 #pragma unroll
@@ -249,6 +243,7 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
       else sf = pow2_neg(ecol[j]);
       const float2 s2 = make_float2(sf, sf);
       uint32_t lo = 0, hi = 0;
+      if (has_rows)
 #pragma unroll
       for (int p = 0; p < 8; p += 2) {
         const float2 y = __fmul2_rn(make_float2(elem(v[p], j), elem(v[p + 1], j)), s2);
@@ -263,11 +258,12 @@ __device__ __forceinline__ void tile_quant_band(const TileQuantParams& P, int64_
 #pragma unroll
     for (int pass = 0; pass < 4; ++pass) {
       const int c = pass * 32 + (t >> 3), h = t & 7;
-      const int64_t cg = c0 + c, rg = B.d0 + 16 * h;
+      const int64_t cg = c0 + c, rg = (RAGGED ? B.d0 : r0) + 16 * h;
       const uint2 a = *(const uint2*)&tq[c * 128 + tq_chunk(c, 2 * h) * 8];
       const uint2 b = *(const uint2*)&tq[c * 128 + tq_chunk(c, 2 * h + 1) * 8];
-      if (cg < P.cols && rg < B.d_ld)
-        *(uint4*)(QC + cg * B.d_ld + rg) = make_uint4(a.x, a.y, b.x, b.y);
+      const int64_t d_ld = RAGGED ? B.d_ld : P.rows;
+      if (cg < P.cols && rg < d_ld)
+        *(uint4*)(QC + cg * d_ld + rg) = make_uint4(a.x, a.y, b.x, b.y);
     }
   }
 }
@@ -310,8 +306,11 @@ __global__ void __launch_bounds__(256, ROWONLY ? 3 : 4) tile_quant_multi_kernel(
 // `per_cta` neighbouring column tiles of one band; each warp finds the band's expert for
 // itself with one scan over the offsets (32 at a time), so nothing is precomputed and the
 // call is one launch.  Bands after the last expert's are written as empty (codes 0, scale 1).
-// The work is the 1x128 quantizer's and so is its bound (bytes); the search costs a load of
-// the offsets before the tile's loads, which per_cta spreads over several tiles.
+// The work is the 1x128 quantizer's and so is its bound, the bytes (those of the padding among
+// them); the search costs a load of the offsets before the tile's loads, which per_cta spreads
+// over several tiles.  (Persistent CTAs with the offsets' table in shared memory, with or without
+// prefetching the next tile into L2, took 138 us where this takes 100: a new CTA's loads overlap
+// the old one's stores, a loop's wait for them.)
 template <bool ROW>
 __global__ void __launch_bounds__(256, 4) tile_quant_grouped_kernel(const __grid_constant__ TileQuantParams P,
                                                                     const int32_t* __restrict__ offs, int groups,
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(256, 4) tile_quant_grouped_kernel(const __grid
   const int64_t band = blockIdx.x / ctas_c;
   const int tc0 = (int)(blockIdx.x % ctas_c) * per_cta;
   const int rows = (int)P.rows;
-  Band B{0, 0, band * 128, bands * 128};
+  Band B{0, 0, band * 128, bands * 128, 0};
   int64_t before = 0;   // bands of the experts scanned so far
   bool bad = false;
   for (int g0 = 0; g0 < groups; g0 += 32) {
@@ -353,16 +352,26 @@ __global__ void __launch_bounds__(256, 4) tile_quant_grouped_kernel(const __grid
     before += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
   if (blockIdx.x == 0 && bad) atomicExch(status, kDevBadArg);
+  if (B.r0 == B.rend) {   // after the last expert: codes 0, scales 1
+    const int c_end = min((tc0 + per_cta) * 128, (int)P.cols), t = threadIdx.x;
+    for (int c = tc0 * 128 + (t >> 3); c < c_end; c += 32)
+      *(uint4*)(P.q_col + (int64_t)c * B.d_ld + B.d0 + 16 * (t & 7)) = make_uint4(0, 0, 0, 0);
+    for (int c = tc0 * 128 + t; c < c_end; c += 256) ((float*)P.s_col)[band * P.ld_s_col + c] = 1.0f;
+    return;
+  }
   for (int i = 0; i < per_cta && tc0 + i < P.tiles_c; ++i) {
     if (i) __syncthreads();   // the staging tile is read before it is written again
-    tile_quant_band<kTile1x128, ROW, true>(P, 0, B, (int64_t)(tc0 + i) * 128, sm);
+    B.c0 = (int64_t)(tc0 + i) * 128;
+    tile_quant_tile<kTile1x128, ROW, true, true>(P, 0, sm, B);
   }
 }
 
 cudaError_t launch_tile_quant_grouped(bool row, const TileQuantParams& p, const int32_t* offs, int groups,
                                       int64_t bands, int num_sms, uint32_t* status, cudaStream_t s) {
   const int64_t tiles = bands * p.tiles_c;
-  const int per_cta = tiles >= 32ll * num_sms ? 4 : 1;   // keep several waves of 4 CTAs per SM
+  // 16384 x 7168 over 32 experts: 106 us with one column tile per CTA, 100 with 2 (5.0 TB/s of the
+  // bytes with the padding), 100 with 4, 107 with 8; few tiles keep all SMs
+  const int per_cta = tiles >= 16ll * num_sms ? 2 : 1;
   const int64_t ctas = bands * ((p.tiles_c + per_cta - 1) / per_cta);
   if (row) tile_quant_grouped_kernel<true><<<dim3((unsigned)ctas), dim3(256), 0, s>>>(p, offs, groups, bands, per_cta, status);
   else tile_quant_grouped_kernel<false><<<dim3((unsigned)ctas), dim3(256), 0, s>>>(p, offs, groups, bands, per_cta, status);
