@@ -312,12 +312,12 @@ fp8q_status fp8q_quantize_1x128_grouped(const void* x, int64_t rows, int64_t col
   if (st != FP8Q_OK) return st;
   if (groups < 1) return FP8Q_ERR_SHAPE;
   if (groups > 256) return FP8Q_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return FP8Q_OK;
   const bool row = q_row || s_row;
   if (!offsets || !q_col || !s_col || (row && (!q_row || !s_row))) return FP8Q_ERR_NULL;
   if (row && (cols % 128 != 0 || ld_s_row < rows || ld_s_row % 4 != 0)) return FP8Q_ERR_SHAPE;
   if (cols % 16 != 0 || ld_s_col < cols || ld_s_col % 4 != 0) return FP8Q_ERR_SHAPE;
   if ((row && !aligned16(q_row)) || !aligned16(q_col)) return FP8Q_ERR_ALIGN;
-  if (rows == 0 || cols == 0) return FP8Q_OK;
   const int64_t bands = fp8q_grouped_capacity(rows, groups) / 128;
   TileQuantParams p{static_cast<const uint16_t*>(x), rows, cols, ld_x, q_row, s_row, ld_s_row,
                     q_col, s_col, ld_s_col, (int)((cols + 127) / 128), 0};

@@ -139,6 +139,20 @@ def test_shared_gradient_counts_twice_and_repeats_exactly(cuda_lib):
     assert float(n1) == float(n2) and torch.equal(o[0], p[0])
 
 
+def test_more_than_four_gigabytes(cuda_lib):
+    """Chunks and offsets past 32 bits: one tensor of 1.2e9 values and a small one."""
+    a = torch.full((1_200_000_003,), 2.0 ** -10, device="cuda")
+    b = torch.ones(5, dtype=B, device="cuda")
+    a[-1] = 3.0
+    norm = cuda_lib.clip_grad_norm([a, b], 1.0)
+    ref = math.sqrt(1_200_000_002 * 2.0 ** -20 + 9.0 + 5.0)
+    coef = 1.0 / (ref + 1e-6)
+    assert abs(float(norm) - ref) <= NORM * ref
+    for got, want in ((a[0], 2.0 ** -10 * coef), (a[1 << 30], 2.0 ** -10 * coef), (a[-2], 2.0 ** -10 * coef), (a[-1], 3 * coef)):
+        assert abs(float(got) - want) <= VALUE[F] * want
+    assert bool((a[:-1] == a[0]).all())
+
+
 def test_graph_and_stream(cuda_lib):
     """Captured with many tensors and replayed on new values, beside an eager call on another stream."""
     ts = [torch.empty(1000 + k, device="cuda") for k in range(100)]

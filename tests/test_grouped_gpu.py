@@ -145,6 +145,51 @@ def test_few_rows_equal_many_rows_to_the_bit(cuda_lib, layout, counts):
         assert torch.equal(one, all_[:M])
 
 
+@pytest.mark.parametrize("extra", [0, 1500])
+@pytest.mark.parametrize("layout", ["fprop", "dgrad"])
+def test_rows_of_other_experts_do_not_leak(cuda_lib, layout, extra):
+    """NaN codes and scales in one expert's rows and matrix leave the others' results alone (in the kernel for few
+    rows and, with many more behind them, in the other)."""
+    fq = cuda_lib
+    counts, K, N = [37, 20, 100 + extra], 256, 144
+    G, M = 3, sum(counts)
+    dgrad = layout == "dgrad"
+    a, b = codes((M, K), 81), codes((G, N, K), 82)
+    sa, sb = scales((2, M + -M % 4), 83), scales((G, 2, 2), 84)
+    call = lambda: fq.gemm(a, b, layout=fq.FP8Q_DGRAD if dgrad else fq.FP8Q_FPROP, a_scale=sa, b_scale=sb,  # noqa: E731
+                           m_offsets=offsets(counts))
+    clean = call()
+    a[37:57] = 0x7F
+    b[1] = 0x7F
+    sa[:, 37:57] = float("nan")
+    sb[1] = float("inf")
+    got = call()
+    assert torch.equal(got[:37], clean[:37]) and torch.equal(got[57:], clean[57:])
+    assert bool(got[37:57].isnan().all())
+
+
+@pytest.mark.parametrize("layout", ["fprop", "dgrad"])
+@pytest.mark.parametrize("offs", [[0, 700, 300, 2000], [0, 700, 9000, 2000], [-3, 700, 900, 2000]])
+def test_many_rows_offsets_out_of_rule(cuda_lib, layout, offs):
+    fq = cuda_lib
+    M, K, N, G = 2000, 256, 144, 3
+    dgrad = layout == "dgrad"
+    a, b, sa, sb = codes((M, K), 91), codes((G, N, K), 92), scales((2, M), 93), scales((G, 2, 2), 94)
+    guard = torch.full((M + 300, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert fq.device_status() == fq.FP8Q_OK
+    fq.gemm(a, b, layout=fq.FP8Q_DGRAD if dgrad else fq.FP8Q_FPROP, a_scale=sa, b_scale=sb,
+            m_offsets=torch.tensor(offs, dtype=torch.int32, device="cuda"), out=guard[:M])
+    assert fq.device_status() == fq.FP8Q_ERR_DEVICE_ARG
+    assert bool((guard[M:] == 7.0).all())
+    clamped = [0]
+    for v in offs[1:]:
+        clamped.append(min(max(v, clamped[-1]), M))
+    counts = [q - p for p, q in zip(clamped, clamped[1:])]
+    n = sum(counts)
+    ref, t = rows_reference(a[:n], sa, b, sb, counts, dgrad)
+    assert_within(guard[:n], ref, gamma(2) * t + 2.0 ** -8 * (ref.abs() + gamma(2) * t), "clamped")
+
+
 def wgrad_reference(x, sx, y, sy, counts):
     c, t, at = [], [], 0
     for n in counts:
@@ -221,6 +266,46 @@ def test_wgrad_offsets_out_of_rule(cuda_lib, offs):
     c = fq.gemm(x, y, fq.FP8Q_BLOCKWISE, fq.FP8Q_WGRAD, a_scale=sx, b_scale=sy, m_offsets=o)
     assert fq.device_status() == fq.FP8Q_ERR_DEVICE_ARG
     assert torch.isfinite(c.float()).all()
+
+
+def test_no_tokens(cuda_lib):
+    """No token at all: BF16 zeros, accumulators and rows as they were."""
+    fq = cuda_lib
+    G, M, N = 3, 48, 64
+    offs = offsets([0, 0, 0])
+    x = torch.zeros((0, M), dtype=torch.bfloat16, device="cuda")
+    q = fq.quantize_1x128_grouped(x, offs)
+    assert q["q_col"].shape == (M, 0) and q["s_col"].shape[0] == 0
+    y = torch.zeros((N, 0), dtype=torch.uint8, device="cuda")
+    sy = torch.zeros((0, N), device="cuda")
+    c = fq.gemm(q["q_col"], y, layout=fq.FP8Q_WGRAD, a_scale=q["s_col"], b_scale=sy, m_offsets=offs)
+    assert c.shape == (G, M, N) and bool((c == 0).all())
+    acc = torch.randn((G, M, N), device="cuda")
+    before = acc.clone()
+    fq.gemm(q["q_col"], y, layout=fq.FP8Q_WGRAD, a_scale=q["s_col"], b_scale=sy, m_offsets=offs, out=acc,
+            accumulate_fp32=True)
+    assert torch.equal(acc, before)
+    b, sb = codes((G, 64, 128), 1), scales((G, 1, 1), 2)
+    r = fq.gemm(torch.zeros((0, 128), dtype=torch.uint8, device="cuda"), b, layout=fq.FP8Q_DGRAD,
+                a_scale=torch.zeros((1, 4), device="cuda"), b_scale=sb, m_offsets=offs)
+    assert r.shape == (0, 64)
+
+
+def test_wgrad_result_past_32_bits(cuda_lib):
+    """C of more than 2^31 elements: its last expert's corner, and its neighbours untouched."""
+    fq = cuda_lib
+    counts, M, N = [128, 0, 200], 24576, 32768          # 3 x 24576 x 32768 = 2.4e9
+    P = fq.fp8q_grouped_capacity(sum(counts), 3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda w: torch.randn((w, P), generator=g, device="cuda").mul_(60).clamp_(-448, 448).to(E4M3).view(torch.uint8)  # noqa: E731
+    x, y = rnd(M), rnd(N)
+    sx, sy = (torch.rand((P // 128, w), generator=g, device="cuda") * 0.01 + 1e-3 for w in (M, N))
+    c = fq.gemm(x, y, layout=fq.FP8Q_WGRAD, a_scale=sx, b_scale=sy, m_offsets=offsets(counts))
+    assert fq.device_status() == fq.FP8Q_OK
+    rows, cols = slice(M - 300, M), slice(N - 300, N)
+    ref, t = wgrad_reference(x[rows], sx[:, rows], y[cols], sy[:, cols], counts)
+    assert_within(c[:, rows, cols], ref, gamma(2) * t + 2.0 ** -8 * (ref.abs() + gamma(2) * t), "far corner")
+    assert bool((c[1] == 0).all())
 
 
 # ------------------------------------------------------------------------------ quantizer
@@ -330,3 +415,90 @@ def test_expert_layer_step(cuda_lib):
             float(x.abs().max() if n else 0) * float(d.abs().max() if n else 0)) * 4 + 1e-6 * before[e].abs()
         assert float(((main[e].double() - before[e]) - x.t() @ d).abs().sub(bound).max()) <= 0
         at += n
+
+
+def test_step_captured_and_replayed_with_other_routing(cuda_lib):
+    """A captured step reads the offsets on the device: replayed with another routing it computes that one, next
+    to the same step run eagerly on another stream."""
+    fq = cuda_lib
+    R, Kin, Nout, G = 600, 256, 384, 4
+    W = workloads.normal_bf16((G, Kin, Nout), 0.02, 5, device="cuda")
+    qw = fq.quantize_128x128_grouped(W)
+    X, dY = torch.empty((R, Kin), dtype=torch.bfloat16, device="cuda"), torch.empty((R, Nout), dtype=torch.bfloat16,
+                                                                                   device="cuda")
+    offs = offsets([R, 0, 0, 0])
+    main = torch.zeros((G, Kin, Nout), device="cuda")
+
+    def step(X, dY, offs, main, stream=None):
+        qx = fq.quantize_1x128_grouped(X, offs, rowwise=True, stream=stream)
+        qy = fq.quantize_1x128_grouped(dY, offs, rowwise=True, stream=stream)
+        y = fq.gemm(qx["q_row"], qw["q_t"], a_scale=qx["s_row"], b_scale=qw["s"], m_offsets=offs, stream=stream)
+        dx = fq.gemm(qy["q_row"], qw["q"], layout=fq.FP8Q_DGRAD, a_scale=qy["s_row"], b_scale=qw["s"], m_offsets=offs,
+                     stream=stream)
+        fq.gemm(qx["q_col"], qy["q_col"], layout=fq.FP8Q_WGRAD, a_scale=qx["s_col"], b_scale=qy["s_col"],
+                m_offsets=offs, out=main, accumulate_fp32=True, stream=stream)
+        return y, dx
+
+    def fill(seed, counts):
+        X.copy_(workloads.normal_bf16((R, Kin), 1.0, seed, device="cuda"))
+        dY.copy_(workloads.normal_bf16((R, Nout), 1e-3, seed + 1, device="cuda"))
+        offs.copy_(offsets(counts))
+        main.zero_()
+
+    fill(1, [R, 0, 0, 0])
+    step(X, dY, offs, main)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, dx = step(X, dY, offs, main)
+    side = torch.cuda.Stream()
+    for seed, counts in ((11, [1, 0, 599, 0]), (21, [150, 151, 149, 150]), (31, [0, 0, 0, 600])):
+        fill(seed, counts)
+        other = [t.clone() for t in (X, dY, offs)]
+        main2 = torch.zeros_like(main)
+        torch.cuda.synchronize()
+        g.replay()
+        with torch.cuda.stream(side):
+            y2, dx2 = step(*other, main2)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(main, main2)
+        qx = fq.quantize_1x128_grouped(X, offs, rowwise=True)
+        ref, t = rows_reference(qx["q_row"], qx["s_row"], qw["q_t"], qw["s"], counts, False)
+        assert_within(y, ref, gamma(2) * t + 2.0 ** -8 * (ref.abs() + gamma(2) * t), "replayed")
+    assert fq.device_status() == fq.FP8Q_OK
+
+
+def test_two_host_threads(cuda_lib):
+    """Two threads, each with its own stream and tensors, get the results of one."""
+    import threading
+    fq = cuda_lib
+    jobs = []
+    for k in range(2):
+        counts = [[40, 90, 3], [200, 0, 700]][k]
+        a, b = codes((sum(counts), 384), 100 + k), codes((3, 256, 384), 200 + k)
+        sa, sb = scales((3, sum(counts) + -sum(counts) % 4), 300 + k), scales((3, 2, 3), 400 + k)
+        x = workloads.normal_bf16((sum(counts), 256), 1.0, 500 + k, device="cuda")
+        jobs.append((a, b, sa, sb, offsets(counts), x))
+
+    def work(job, out):
+        a, b, sa, sb, offs, x = job
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                c = fq.gemm(a, b, a_scale=sa, b_scale=sb, m_offsets=offs)
+                q = fq.quantize_1x128_grouped(x, offs)
+                n = fq.clip_grad_norm([x], 1.0, out=[torch.empty_like(x)])
+            torch.cuda.current_stream().synchronize()
+        out += [c, q["q_col"], q["s_col"], n]
+
+    alone = [[] for _ in jobs]
+    for j, o in zip(jobs, alone):
+        work(j, o)
+    both = [[] for _ in jobs]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(j, o)) for j, o in zip(jobs, both)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    for p, q in zip(alone, both):
+        assert len(q) == 4 and all(torch.equal(u, v) for u, v in zip(p, q))

@@ -1,8 +1,9 @@
 """The norms around a block, its gate and residual scale, and their gradients, against 64 bits.
 
 Tolerances, with u = 2^-24 (one FP32 rounding).  A row sum adds at most 32 terms per thread, 5
-lanes' levels and 16 warps, so its error is at most 54 u of the sum of magnitudes (one more u for
-each term): rms(y), half of that and four roundings more, is within 32 u of itself, and
+levels over a warp and 5 over up to 16 warps, so with one more rounding per term its error is below
+54 u of the sum of magnitudes: rms(y), half of that and four roundings more, is within 32 u of
+itself, and
   h' = alpha h + gate z   is within  E_h = u (2 |alpha h| + 40 |gate z|),
   rms(h')                 within     32 u + ||E_h|| / ||h'||  of itself (it moves with the norm of h'),
   n                       within     E_n = |w_pre| rms(h') E_h + (36 u + ||E_h|| / ||h'||) |n|.
@@ -250,6 +251,39 @@ def test_backward_against_differences(cuda_lib, post, gate):
         # the kernel's h' is rounded (FP32) where the formula's is not: 40 u of every term more
         slack = float(((e + (half + 400 * U) * val.abs()) * v.abs()).sum()) + 1e-6 * float((val * v).abs().sum())
         assert abs(diff - float((o[grad].double() * v).sum())) <= slack, name
+
+
+@pytest.mark.parametrize("C", [256, 3200, 4096, 7168, 8200, 16384])
+def test_a_row_does_not_depend_on_the_others(cuda_lib, C):
+    """The same row among 3 and among 500 rows, to the bit, forward and backward."""
+    fq = cuda_lib
+    x = inputs(500, C, F, B, True, True, seed=7)
+    r = fq.norm_residual(x["y"], x["h"], x["w_pre"], x["w_post"], x["gate"], quantize=C % 128 == 0)
+    few = {k: v[:3] if v is not None and v.dim() == 2 else v for k, v in x.items()}
+    rf = fq.norm_residual(few["y"], few["h"], x["w_pre"], x["w_post"], x["gate"], quantize=C % 128 == 0)
+    for k in ("h", "n", "rstd_pre", "rstd_post") + (("q_row",) if C % 128 == 0 else ()):
+        assert torch.equal(r[k][:3], rf[k]), k
+    o = run_backward(fq, {**x, "h": r["h"]}, r, 1.0)
+    of = run_backward(fq, {**few, "h": rf["h"]}, rf, 1.0)
+    assert torch.equal(o["dh"][:3], of["dh"]) and torch.equal(o["dy"][:3], of["dy"])
+
+
+def test_more_than_2_31_values(cuda_lib):
+    """Rows past 32-bit element offsets equal the same rows alone."""
+    R, C = 270_000, 8192                                   # 2.2e9 values
+    y = torch.randn((64, C), device="cuda").to(B).repeat(R // 64 + 1, 1)[:R]
+    h = torch.randn((64, C), device="cuda").to(B).repeat(R // 64 + 1, 1)[:R]
+    w = torch.ones(C, dtype=B, device="cuda")
+    o = cuda_lib.norm_residual(y, h, w, w, None, normed=False, quantize=True)
+    few = cuda_lib.norm_residual(y[-200:], h[-200:], w, w, None, normed=False, quantize=True)
+    assert torch.equal(o["q_row"][-200:], few["q_row"]) and torch.equal(o["h"][-200:], few["h"])
+    assert torch.equal(o["s_row"][:, R - 200:R], few["s_row"][:, :200])
+    del o
+    dn = y
+    g = cuda_lib.norm_residual_backward(dn, h, y, h, torch.ones(R, device="cuda"), w, alpha=0.5)
+    last = cuda_lib.norm_residual_backward(dn[-200:], h[-200:], y[-200:], h[-200:], torch.ones(200, device="cuda"), w,
+                                           alpha=0.5)
+    assert torch.equal(g["dh"][-200:], last["dh"]) and torch.equal(g["dy"][-200:], last["dy"])
 
 
 def test_graph_beside_an_eager_call(cuda_lib):
