@@ -707,9 +707,9 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
     o = {"h": h_out, "rstd_pre": torch.empty((R,), dtype=torch.float32, device=dev),
          "rstd_post": None if w_post is None else torch.empty((R,), dtype=torch.float32, device=dev)}
     if normed:
-        o["n"] = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+        o["n"] = torch.empty_like(y, memory_format=torch.contiguous_format)
     if quantize:
-        o["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        o["q_row"] = torch.empty_like(y, dtype=torch.uint8, memory_format=torch.contiguous_format)
         o["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
     a = NormArgs(R, C, hd, wd, alpha, eps, y.data_ptr(), _ld(y), h.data_ptr(), _ld(h), _addr(w_post), _addr(gate),
                  w_pre.data_ptr(), h_out.data_ptr(), _ld(h_out), _addr(o.get("n")), C, _addr(o.get("q_row")),
@@ -737,8 +737,8 @@ def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post
     R, C = y.shape
     dev = y.device
     vec = lambda: torch.empty((C,), dtype=torch.float32, device=dev)  # noqa: E731
-    o = {"dh": torch.empty((R, C), dtype=h.dtype, device=dev), "dy": torch.empty((R, C), dtype=torch.bfloat16, device=dev),
-         "dw_pre": vec()}
+    o = {"dh": torch.empty_like(h, memory_format=torch.contiguous_format),
+         "dy": torch.empty_like(y, memory_format=torch.contiguous_format), "dw_pre": vec()}
     if w_post is not None:
         o["dw_post"] = vec()
     if gate is not None:
@@ -783,12 +783,13 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
     words[2::4], words[3::4] = sizes, types
     items = array.array("q", words)
     nbytes = fp8q_clip_grad_workspace_bytes(len(grads))
-    ws = torch.empty(nbytes + 16, dtype=torch.uint8, device=dev)     # the norm after the partial sums
-    norm = ws[nbytes:nbytes + 4].view(torch.float32)[0]
+    ws = torch.empty(nbytes // 4 + 1, dtype=torch.float32, device=dev)     # the norm after the partial sums
+    norm, base = ws[nbytes // 4], ws.data_ptr()
     if stream is not None:
         ws.record_stream(stream)
     with _on(dev, stream):
-        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps, _ptr(norm), _ptr(ws), nbytes, _stream(stream))
+        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps, ctypes.c_void_p(base + nbytes),
+                                 ctypes.c_void_p(base), nbytes, _stream(stream))
     _check(st, "fp8q_clip_grad_norm")
     return norm
 

@@ -128,8 +128,16 @@ struct Weights {
   }
 };
 
-__device__ __forceinline__ float rms_factor(float sum, int cols, float eps) {
-  return 1.0f / sqrtf(sum / (float)cols + eps);
+__device__ __forceinline__ float rms_factor(float sum, float inv_cols, float eps) {
+  return __frsqrt_rn(fmaf(sum, inv_cols, eps));
+}
+
+// Sum of the thread's NV parts (one chain of dependent additions per part keeps them short).
+template <int NV>
+__device__ __forceinline__ float add_parts(const float (&v)[NV]) {
+  if constexpr (NV == 4) return (v[0] + v[1]) + (v[2] + v[3]);
+  else if constexpr (NV == 2) return v[0] + v[1];
+  else return v[0];
 }
 
 }  // namespace
@@ -165,6 +173,7 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
     }
   Weights<NV, W32, true> W;
   W.init(p, tid, T);
+  const float inv_c = 1.0f / (float)C;
   uint32_t it = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += step, ++it) {
     const int s = it % p.stages;
@@ -173,23 +182,25 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
     const uint8_t* hs = ys + ybytes;
     float rq = 1.0f;
     if (post) {
-      float ss = 0.0f;
+      float ss[NV];
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int col = (v * T + tid) * 8;
+        ss[v] = 0.0f;
         if (col < C) {
           float y[8];
           get8<false>(ys, col, y);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
+          for (int k = 0; k < 8; ++k) ss[v] = fmaf(y[k], y[k], ss[v]);
         }
       }
-      rq = rms_factor(row_sum(ss, sh.sums[0], ok), C, p.eps);
+      rq = rms_factor(row_sum(add_parts(ss), sh.sums[0], ok), inv_c, p.eps);
     }
-    float x[NV][8], ss = 0.0f;
+    float x[NV][8], ss[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (v * T + tid) * 8;
+      ss[v] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[v][k] = 0.0f;
       if (col < C) {
@@ -200,11 +211,11 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           x[v][k] = fmaf(p.alpha, h[k], y[k] * rq * w[k]);
-          ss = fmaf(x[v][k], x[v][k], ss);
+          ss[v] = fmaf(x[v][k], x[v][k], ss[v]);
         }
       }
     }
-    const float rp = rms_factor(row_sum(ss, sh.sums[post ? 1 : it & 1], ok), C, p.eps);
+    const float rp = rms_factor(row_sum(add_parts(ss), sh.sums[post ? 1 : it & 1], ok), inv_c, p.eps);
     if (!ok) break;
     // every thread has read the stage
     if (tid == 0 && row + p.stages * step < p.rows) {
@@ -323,10 +334,11 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
     const uint8_t* dhs = hs + hbytes;
     const uint8_t* ys = dhs + hbytes;
     const float rp = p.rstd_pre[row], rq = post ? p.rstd_post[row] : 1.0f;
-    float c1 = 0.0f;
+    float part[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (v * T + tid) * 8;
+      part[v] = 0.0f;
       if (col < C) {
         float dn[8], h[8], w[8];
         get8<false>(dns, col, dn);
@@ -336,23 +348,24 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         for (int k = 0; k < 8; ++k) {
           const float t = dn[k] * (h[k] * rp);
           acc_pre[v][k] += t;
-          c1 = fmaf(t, w[k], c1);
+          part[v] = fmaf(t, w[k], part[v]);
         }
       }
     }
-    c1 = row_sum(c1, sh.sums[post ? 0 : j & 1], ok) * inv_c;
+    const float c1 = row_sum(add_parts(part), sh.sums[post ? 0 : j & 1], ok) * inv_c;
     if (!ok) break;
     // every thread has left row j - 1: its stage's remaining parts may be refilled
     if (tid == 0 && j > 0) {
       if (!post) load_a(j - 1 + S);
       load_y(j - 1 + S);
     }
-    float d[NV][8], c2 = 0.0f;
+    float d[NV][8];
     uint8_t* dh = static_cast<uint8_t*>(p.dh) + row * p.ld_dh * HB;
     uint8_t* dy = static_cast<uint8_t*>(p.dy) + row * p.ld_dy * 2;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (v * T + tid) * 8;
+      part[v] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[v][k] = 0.0f;
       if (col < C) {
@@ -375,13 +388,13 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           d[v][k] *= w[k];
-          c2 = fmaf(d[v][k], y[k] * rq, c2);
+          part[v] = fmaf(d[v][k], y[k] * rq, part[v]);
         }
         if (!post) put8<false>(dy, col, d[v]);
       }
     }
     if (post) {
-      c2 = row_sum(c2, sh.sums[1], ok) * inv_c;
+      const float c2 = row_sum(add_parts(part), sh.sums[1], ok) * inv_c;
       if (tid == 0) load_a(j + S);   // dn, h', dh' of row j have been read by every thread
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -427,6 +440,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
   const int C = p.cols, col = blockIdx.x * 32 + tx;
   float a = 0.0f, b = 0.0f;
   if (col < C)
+#pragma unroll 8
     for (int k = ty; k < ctas; k += 8) {
       const float* part = p.partials + (int64_t)k * 2 * C + col;
       a += part[0];
