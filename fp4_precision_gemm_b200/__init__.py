@@ -576,6 +576,20 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
     if grouped and not k_groups and (b.shape[0] != groups or b.stride(0) != b.shape[1] * b.stride(1)):
         raise ValueError("b must hold one matrix per expert, one directly after the other")
     N = b.shape[-2]
+    if grouped and recipe == FP8Q_BLOCKWISE:
+        # the kernels read whole tiles of scales at these strides: a wrong shape would read past them
+        kb, nb, rows = a.shape[1] // 128, -(-N // 128), M
+        want = (kb, N) if k_groups else (groups, kb, nb) if layout == FP8Q_DGRAD else (groups, nb, kb)
+        if a.shape[1] != b.shape[-1]:
+            raise ValueError("a and b must have the same K")
+        if (a_scale is not None and ld_sa is None
+                and (a_scale.dim() != 2 or a_scale.shape[0] < kb or a_scale.shape[1] < rows
+                     or not a_scale.is_contiguous())):
+            raise ValueError("a_scale must be contiguous, (K/128, M or more)")
+        if (b_scale is not None and ld_sb is None
+                and (b_scale.dim() != len(want) or not b_scale.is_contiguous()
+                     or (b_scale.shape[0] < kb or b_scale.shape[1] < N if k_groups else tuple(b_scale.shape) != want))):
+            raise ValueError(f"b_scale must be contiguous, {want}" + (" or more" if k_groups else ""))
     if K is None:
         K = a.shape[1] * (2 if recipe == FP8Q_NVFP4 else 1)
     if accumulate_fp32 and (out is None or out.dtype != torch.float32):

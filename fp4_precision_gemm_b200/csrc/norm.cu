@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
     const float c1 = row_sum(add_parts(part), sh.sums[post ? 0 : j & 1], ok) * inv_c;
     if (!ok) break;
     // every thread has left row j - 1: its stage's remaining parts may be refilled
-    if (tid == 0 && j > 0) {
+    if (tid == 0 && j > 0 && S > 1) {
       if (!post) load_a(j - 1 + S);
       load_y(j - 1 + S);
     }
@@ -408,14 +408,22 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         }
       }
     }
+    if (S == 1) {   // wide rows: the only stage is refilled when every thread has left this row
+      __syncthreads();
+      if (tid == 0) {
+        if (!post) load_a(j + 1);
+        load_y(j + 1);
+      }
+    }
   }
   if (!ok) {   // gave up at row j: report, and leave no copy in flight
     if (tid == 0) {
       atomicExch(p.status, kDevTimeout);
+      const int late = j > 0 && S > 1;   // the parts of row j - 1 + S are not on their way yet
       for (int64_t i = j; i < j + S && i < mine; ++i) {
         const uint32_t ph = (uint32_t)(i / S) & 1;
-        if (i < j + S - (!post && j > 0)) mbar_wait_drain(&full_a[i % S], ph, kNormWaitNs);
-        if (i < j + S - (j > 0)) mbar_wait_drain(&full_y[i % S], ph, kNormWaitNs);
+        if (i < j + S - (post ? 0 : late)) mbar_wait_drain(&full_a[i % S], ph, kNormWaitNs);
+        if (i < j + S - late) mbar_wait_drain(&full_y[i % S], ph, kNormWaitNs);
       }
     }
     return;

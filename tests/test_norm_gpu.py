@@ -87,7 +87,7 @@ def check_forward(x, o, alpha, eps, hd):
 
 
 SHAPES = [(1, 8), (3, 256), (1, 16384), (5, 7168), (2, 16376), (700, 128), (333, 1000), (64, 4096), (150, 4104),
-          (301, 8192), (149, 8200)]
+          (301, 8192), (149, 8200), (450, 9344), (450, 9352), (310, 14336), (460, 16384)]
 
 
 @pytest.mark.parametrize("post,gate", [(True, True), (True, False), (False, True), (False, False)])

@@ -96,6 +96,15 @@ def test_grouped_gemm_binding_refusals():
         fq.gemm(a, b[0], layout=fq.FP8Q_WGRAD, m_offsets=offs, out=torch.zeros((2, 8, 64)), accumulate_fp32=True)
     with pytest.raises(ValueError):
         fq.gemm(a, b, m_offsets=offs[::2])
+    sa, sb = torch.ones((1, 8)), torch.ones((2, 1, 1))
+    for bad in (dict(a_scale=torch.ones((1, 4)), b_scale=sb), dict(a_scale=torch.ones(8), b_scale=sb),
+                dict(a_scale=sa, b_scale=torch.ones((1, 1, 1))), dict(a_scale=sa, b_scale=torch.ones((2, 1, 2))),
+                dict(a_scale=torch.ones((1, 16))[:, ::2], b_scale=sb)):
+        with pytest.raises(ValueError):
+            fq.gemm(a, b, m_offsets=offs, **bad)
+    with pytest.raises(ValueError):                                          # wgrad: scales of too few chunks
+        fq.gemm(torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((16, 256), dtype=torch.uint8),
+                layout=fq.FP8Q_WGRAD, a_scale=torch.ones((1, 8)), b_scale=torch.ones((2, 16)), m_offsets=offs)
 
 
 def items(*rows):
