@@ -457,11 +457,11 @@ def quantize_1x128_grouped(x, m_offsets, rowwise=False, colwise=True, stream=Non
     groups = m_offsets.numel() - 1
     P = fp8q_grouped_capacity(R, groups)
     dev = x.device
-    out = {"q_col": torch.empty((C, P), dtype=torch.uint8, device=dev),
-           "s_col": torch.empty((P // 128, C + (-C) % 4), dtype=torch.float32, device=dev)}
+    out = {"q_col": x.new_empty((C, P), dtype=torch.uint8),
+           "s_col": x.new_empty((P // 128, C + (-C) % 4), dtype=torch.float32)}
     if rowwise:
-        out["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-        out["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
+        out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
+        out["s_row"] = x.new_empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32)
     with _on(dev, stream):
         st = fp8q_quantize_1x128_grouped(_ptr(x), R, C, x.stride(0), _ptr(m_offsets), groups, _ptr(out.get("q_row")),
                                          _ptr(out.get("s_row")), out["s_row"].shape[1] if rowwise else 0,
@@ -672,36 +672,19 @@ def gemm_workspace_bytes(M, N, K, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, accu
 _DTYPES = {torch.bfloat16: FP8Q_BF16, torch.float32: FP8Q_FP32}
 
 
-def _norm_operands(y, h, w_pre, w_post, gate, like_y=(), like_h=(), rows=()):
-    """Checks the tensors of a norm call; returns (h_dtype, w_dtype).  like_y / like_h: further matrices of y's
-    type and of h's; rows: float32 vectors with one value per row."""
-    _check_bf16(y, "y")
-    R, C = y.shape
-    if h.dtype not in _DTYPES or w_pre.dtype not in _DTYPES:
-        raise ValueError("h and the weights must be bfloat16 or float32")
-    index, shape, hd, wd = y.get_device(), y.shape, h.dtype, w_pre.dtype
-    for t in (h, *like_y, *like_h):
-        if t.shape != shape or t.get_device() != index or t.stride(1) != 1:
-            raise ValueError("matrices must be row-major, of y's shape and on its device")
-    for t in like_y:
-        if t.dtype != torch.bfloat16:
-            raise ValueError("matrices of y's kind must be bfloat16")
-    for t in like_h:
-        if t.dtype != hd:
-            raise ValueError("matrices of h's kind must be of h's type")
-    for t in (w_pre, w_post, gate):
-        if t is not None and (t.dtype != wd or t.get_device() != index or t.dim() != 1 or t.numel() != C
-                              or not t.is_contiguous()):
-            raise ValueError("w_pre, w_post and gate must be contiguous vectors of y's columns, of one type")
-    for t in rows:
-        if (t.dtype != torch.float32 or t.get_device() != index or t.dim() != 1 or t.numel() != R
-                or not t.is_contiguous()):
-            raise ValueError("rstd vectors must be contiguous float32, one value per row")
-    return _DTYPES[h.dtype], _DTYPES[w_pre.dtype]
+def _matrix(t, dtype, shape, index):
+    """Checks a norm call's matrix; returns its row stride (a single row has the columns': its own means nothing)."""
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or strides[1] != 1:
+        raise ValueError(f"matrices must be row-major, of y's shape and on its device; this one must be {dtype}")
+    return strides[0] if shape[0] > 1 else shape[1]
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _vector(t, dtype, n, index):
+    if (t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or t.numel() != n
+            or not t.is_contiguous()):
+        raise ValueError(f"expected a contiguous {dtype} vector of {n} on y's device")
+    return t.data_ptr()
 
 
 def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, normed=True, quantize=False, out=None,
@@ -712,31 +695,42 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
     `out` if given, which may be h itself), n (R, C) bfloat16 if `normed`, q_row and s_row (the 1x128
     quantization of n, laid out as quantize_1x128 does) if `quantize`, and rstd_pre, rstd_post (R,) float32 for
     norm_residual_backward (rstd_post None without w_post)."""
-    h_out = torch.empty_like(h, memory_format=torch.contiguous_format) if out is None else out
-    hd, wd = _norm_operands(y, h, w_pre, w_post, gate, like_h=(h_out,))
+    _check_bf16(y, "y")
+    shape, index, dev, hd, wd = y.shape, y.get_device(), y.device, h.dtype, w_pre.dtype
+    R, C = shape
+    if hd not in _DTYPES or wd not in _DTYPES:
+        raise ValueError("h and the weights must be bfloat16 or float32")
     if not (normed or quantize):
         raise ValueError("neither output of the norm is asked for")
-    R, C = y.shape
-    dev = y.device
-    o = {"h": h_out, "rstd_pre": torch.empty((R,), dtype=torch.float32, device=dev),
-         "rstd_post": None if w_post is None else torch.empty((R,), dtype=torch.float32, device=dev)}
+    ld_y, ld_h = _matrix(y, torch.bfloat16, shape, index), _matrix(h, hd, shape, index)
+    p_pre = _vector(w_pre, wd, C, index)
+    p_post = None if w_post is None else _vector(w_post, wd, C, index)
+    p_gate = None if gate is None else _vector(gate, wd, C, index)
+    if out is None:
+        out, ld_out = torch.empty_like(h, memory_format=torch.contiguous_format), C
+    else:
+        ld_out = _matrix(out, hd, shape, index)
+    rstd = y.new_empty((R,), dtype=torch.float32)
+    rstd_post = None if w_post is None else y.new_empty((R,), dtype=torch.float32)
+    o = {"h": out, "rstd_pre": rstd, "rstd_post": rstd_post}
+    n = q = sc = None
+    ld_s = 0
     if normed:
-        o["n"] = torch.empty_like(y, memory_format=torch.contiguous_format)
+        o["n"] = n = torch.empty_like(y, memory_format=torch.contiguous_format)
     if quantize:
-        o["q_row"] = torch.empty_like(y, dtype=torch.uint8, memory_format=torch.contiguous_format)
-        o["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
-    a = NormArgs(R, C, hd, wd, alpha, eps, y.data_ptr(), _ld(y), h.data_ptr(), _ld(h), _addr(w_post), _addr(gate),
-                 w_pre.data_ptr(), h_out.data_ptr(), _ld(h_out), _addr(o.get("n")), C, _addr(o.get("q_row")),
-                 _addr(o.get("s_row")), o["s_row"].shape[1] if quantize else 0, _addr(o["rstd_post"]),
-                 o["rstd_pre"].data_ptr())
+        ld_s = max(R, 1) + (-max(R, 1)) % 4
+        o["q_row"] = q = torch.empty_like(y, dtype=torch.uint8, memory_format=torch.contiguous_format)
+        o["s_row"] = sc = y.new_empty((C // 128, ld_s), dtype=torch.float32)
+    a = NormArgs(R, C, _DTYPES[hd], _DTYPES[wd], alpha, eps, y.data_ptr(), ld_y, h.data_ptr(), ld_h, p_post, p_gate,
+                 p_pre, out.data_ptr(), ld_out, _addr(n), C, _addr(q), _addr(sc), ld_s, _addr(rstd_post),
+                 rstd.data_ptr())
     with _on(dev, stream):
         _check(fp8q_norm_residual(a, _stream(stream)), "fp8q_norm_residual")
     return o
 
 
-def _ld(t):
-    """Row stride of a row-major matrix; a single row has the columns' (its own stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post=None, gate=None, alpha=1.0,
@@ -744,28 +738,38 @@ def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post
     """Gradients of norm_residual from dn (of n, bfloat16) and dh (of h', of h's type); y, w_pre, w_post, gate and
     alpha as given to it, h, rstd_pre and rstd_post as it returned them.  Returns dh (of the incoming residual),
     dy (bfloat16), and float32 dw_pre, with w_post dw_post, with gate dgate (C,)."""
+    _check_bf16(y, "y")
+    shape, index, dev, hd, wd = y.shape, y.get_device(), y.device, h.dtype, w_pre.dtype
+    R, C = shape
+    if hd not in _DTYPES or wd not in _DTYPES:
+        raise ValueError("h and the weights must be bfloat16 or float32")
     if (w_post is None) != (rstd_post is None):
         raise ValueError("w_post and rstd_post go together")
-    hd, wd = _norm_operands(y, h, w_pre, w_post, gate, like_y=(dn,), like_h=(dh,),
-                            rows=(rstd_pre,) if rstd_post is None else (rstd_pre, rstd_post))
-    R, C = y.shape
-    dev = y.device
-    vec = lambda: torch.empty((C,), dtype=torch.float32, device=dev)  # noqa: E731
-    o = {"dh": torch.empty_like(h, memory_format=torch.contiguous_format),
-         "dy": torch.empty_like(y, memory_format=torch.contiguous_format), "dw_pre": vec()}
+    ld_dn, ld_y = _matrix(dn, torch.bfloat16, shape, index), _matrix(y, torch.bfloat16, shape, index)
+    ld_dh, ld_h = _matrix(dh, hd, shape, index), _matrix(h, hd, shape, index)
+    p_rstd, p_pre = _vector(rstd_pre, torch.float32, R, index), _vector(w_pre, wd, C, index)
+    p_post = p_rstd_post = p_gate = None
+    names = ["dw_pre"]
     if w_post is not None:
-        o["dw_post"] = vec()
+        p_post, p_rstd_post = _vector(w_post, wd, C, index), _vector(rstd_post, torch.float32, R, index)
+        names.append("dw_post")
     if gate is not None:
-        o["dgate"] = vec()
+        p_gate = _vector(gate, wd, C, index)
+        names.append("dgate")
+    dh_in = torch.empty_like(h, memory_format=torch.contiguous_format)
+    dy = torch.empty_like(y, memory_format=torch.contiguous_format)
+    sums = y.new_empty((len(names), C), dtype=torch.float32)      # one allocation for the vectors
+    o = {"dh": dh_in, "dy": dy, **dict(zip(names, sums.unbind(0)))}
+    at = dict(zip(names, range(sums.data_ptr(), sums.data_ptr() + 4 * C * len(names), 4 * C)))
     with _on(dev, stream):
-        nbytes = fp8q_norm_backward_workspace_bytes(R, C, hd)
-        ws = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        nbytes = fp8q_norm_backward_workspace_bytes(R, C, _DTYPES[hd])
+        ws = y.new_empty((max(nbytes, 16),), dtype=torch.uint8)
         if stream is not None:
             ws.record_stream(stream)
-        a = NormBackwardArgs(R, C, hd, wd, alpha, dn.data_ptr(), _ld(dn), dh.data_ptr(), _ld(dh), y.data_ptr(), _ld(y),
-                             h.data_ptr(), _ld(h), _addr(w_post), _addr(gate), w_pre.data_ptr(), _addr(rstd_post),
-                             rstd_pre.data_ptr(), o["dh"].data_ptr(), C, o["dy"].data_ptr(), C, _addr(o.get("dw_post")),
-                             _addr(o.get("dgate")), o["dw_pre"].data_ptr(), ws.data_ptr(), nbytes)
+        a = NormBackwardArgs(R, C, _DTYPES[hd], _DTYPES[wd], alpha, dn.data_ptr(), ld_dn, dh.data_ptr(), ld_dh,
+                             y.data_ptr(), ld_y, h.data_ptr(), ld_h, p_post, p_gate, p_pre, p_rstd_post, p_rstd,
+                             dh_in.data_ptr(), C, dy.data_ptr(), C, at.get("dw_post"), at.get("dgate"), at["dw_pre"],
+                             ws.data_ptr(), nbytes)
         _check(fp8q_norm_residual_backward(a, _stream(stream)), "fp8q_norm_residual_backward")
     return o
 
@@ -783,18 +787,18 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
         raise ValueError("out must have one tensor per gradient")
     # whole lists at a time: hundreds of tensors are usual, and a loop of checks costs microseconds each
     dev, index, n = grads[0].device, grads[0].get_device(), len(grads)
-    types, sizes = [_DTYPES.get(g.dtype) for g in grads], [g.numel() for g in grads]
-    if (index < 0 or None in types or [g.get_device() for g in grads].count(index) != n
+    kinds, sizes = [g.dtype for g in grads], [g.numel() for g in grads]
+    if (index < 0 or not _DTYPES.keys() >= set(kinds) or [g.get_device() for g in grads].count(index) != n
             or False in [g.is_contiguous() for g in grads]):
         raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
-    if out is not None and ([_DTYPES.get(o.dtype) for o in outs] != types or [o.numel() for o in outs] != sizes
+    if out is not None and ([o.dtype for o in outs] != kinds or [o.numel() for o in outs] != sizes
                             or [o.get_device() for o in outs].count(index) != n
                             or False in [o.is_contiguous() for o in outs]):
         raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
     words = [0] * (4 * n)                                  # GradItem is four 64-bit words
     words[0::4] = [g.data_ptr() for g in grads]
     words[1::4] = words[0::4] if out is None else [o.data_ptr() for o in outs]
-    words[2::4], words[3::4] = sizes, types
+    words[2::4], words[3::4] = sizes, [_DTYPES[k] for k in kinds]
     items = array.array("q", words)
     nbytes = fp8q_clip_grad_workspace_bytes(len(grads))
     ws = torch.empty(nbytes // 4 + 1, dtype=torch.float32, device=dev)     # the norm after the partial sums
