@@ -28,7 +28,8 @@
  *   - The library allocates no device memory for tensors.  Calls that need a global amax
  *     (per-tensor and NVFP4 quantization) and the status word use a small per-device
  *     scratch pool the library allocates on first use and keeps until
- *     fp8q_release_scratch() or process exit.
+ *     fp8q_release_scratch() or process exit.  That allocation is not allowed while a stream is
+ *     captured into a graph: make a first call (fp8q_get_device_status will do) before.
  *
  * Quantization rules (the readings the pages leave open, shared by the CPU oracle):
  *   E4M3 is OCP "E4M3FN" (max 448), encoded round-to-nearest-even with saturation.
