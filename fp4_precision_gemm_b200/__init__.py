@@ -596,8 +596,11 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
         raise ValueError("accumulate_fp32 needs an FP32 `out` tensor to update")
     shape = (groups, M, N) if k_groups else (M, N)
     c = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=a.device)
-    if k_groups and (tuple(c.shape) != shape or c.stride(2) != 1 or c.stride(0) != M * c.stride(1)):
-        raise ValueError("grouped WGRAD `out` must be (G, M, N), one matrix directly after the other")
+    if grouped and (c.dtype != (torch.float32 if accumulate_fp32 else torch.bfloat16) or tuple(c.shape) != shape
+                    or c.stride(-1) != 1):
+        raise ValueError(f"grouped `out` must be row-major {shape}, bfloat16 or, with accumulate_fp32, float32")
+    if k_groups and c.stride(0) != M * c.stride(1):
+        raise ValueError("grouped WGRAD `out` must hold one matrix directly after the other")
     args = GemmArgs()
     args.recipe, args.layout = recipe, layout
     args.M, args.N, args.K = M, N, K

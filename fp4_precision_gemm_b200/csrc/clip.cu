@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
   for (int k = threadIdx.x; k < n_partials; k += kThreads) t += partials[k];
   const double norm = sqrt(block_sum(t, sh));
   const double ratio = max_norm / (norm + eps);
-  const float coef = ratio >= 1.0 ? 1.0f : (float)ratio;   // a NaN norm gives a NaN factor
+  // no limit: the norm only; else a NaN norm gives a NaN factor
+  const float coef = isinf(max_norm) || ratio >= 1.0 ? 1.0f : (float)ratio;
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   if (in_place && coef == 1.0f) return;                    // 1 * g is g: nothing to write
   int c = P.chunk_begin[P.n] - 1 - (int)blockIdx.x;

@@ -397,7 +397,10 @@ typedef enum { FP8Q_BF16 = 0, FP8Q_FP32 = 1 } fp8q_dtype;
  * fp8q_quantize_1x128 lays them out, cols % 128 == 0, ld_s_row >= rows, % 4 == 0, made from n in
  * FP32), at least one; rstd_pre and rstd_post (rows floats: rms(h'), rms(y)), each optional.
  * 1 <= cols <= 16384, cols % 8 == 0; leading dimensions (elements) >= cols, % 8 == 0; pointers of
- * matrices, weights and the gate 16-byte aligned; eps >= 0 and finite.  rows == 0 -> FP8Q_OK. */
+ * matrices, weights and the gate 16-byte aligned; eps >= 0 and finite.  rows == 0 -> FP8Q_OK.
+ * A row's results depend on that row only, to the bit.  Outputs overlap no input (but h_out may be
+ * h, with the same leading dimension) and not each other.  Squares are formed in FP32: magnitudes
+ * from about 1e-19 to 1e17 are safe. */
 typedef struct {
   int64_t rows, cols;
   int32_t h_dtype, w_dtype;    /* fp8q_dtype of h / h_out, and of w_pre / w_post / gate */
@@ -429,7 +432,8 @@ fp8q_status fp8q_norm_residual(const fp8q_norm_args* args, void* stream);
  *   b = d gate w_post,  dy = rstd_post (b - yh mean(b yh))      (BF16; without w_post: d gate)
  *   dw_pre = sum over rows of dn xh,  dgate = w_post * S,  dw_post = gate * S,  S = sum of d yh
  * dh, dy and dw_pre are required; dw_post (needs w_post) and dgate (needs gate) are optional;
- * these three are cols floats each, overwritten.  Row sums and column sums are FP32, added in an
+ * these three are cols floats each, overwritten.  Outputs overlap no input (but dh may be dh_out,
+ * with the same leading dimension) and not each other.  Row sums and column sums are FP32, added in an
  * order that depends only on the sizes and the device, so results repeat exactly.
  * workspace: device memory, 16-byte aligned, fp8q_norm_backward_workspace_bytes(rows, cols,
  * h_dtype) bytes, used by the call's two kernels only.  The forward call's limits hold;
@@ -479,8 +483,8 @@ size_t fp8q_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t h_
  * FP32's range; the factor is formed in FP64); with no elements it is 0.
  * Sums are formed in FP64 (finite gradients of any size give the correct norm) in an order that
  * depends only on the sizes, alignments and the device, so results repeat exactly.  A norm of NaN
- * makes every clipped value NaN; one of infinity makes the factor 0.  max_norm >= 0 (not NaN),
- * eps >= 0 and finite.
+ * makes every clipped value NaN; one of infinity makes the factor 0.  max_norm >= 0 (not NaN);
+ * infinity takes the norm only (the factor is 1 whatever the norm).  eps >= 0 and finite.
  * workspace: device memory, 16-byte aligned, of fp8q_clip_grad_workspace_bytes(n_items) bytes,
  * used by the call's kernels only (not concurrently elsewhere).  Asynchronous on `stream`, one
  * norm and one scaling launch per 1024 items. */

@@ -114,6 +114,12 @@ def test_nan_and_infinity(cuda_lib):
     b[7] = float("nan")
     assert math.isnan(float(cuda_lib.clip_grad_norm([a, b], 1.0)))
     assert bool(a.isnan().all()) and bool(b.isnan().all())
+    for bad in (float("nan"), float("inf")):                   # no limit: the norm only, whatever it is
+        a = torch.ones(100, device="cuda")
+        a[3] = bad
+        before = a.clone()
+        assert not math.isfinite(float(cuda_lib.clip_grad_norm([a], math.inf)))
+        assert torch.equal(a.view(torch.int32), before.view(torch.int32))
     a = torch.ones(100, device="cuda")
     a[3] = float("inf")
     assert float(cuda_lib.clip_grad_norm([a], 1.0)) == math.inf

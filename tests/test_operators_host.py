@@ -102,6 +102,10 @@ def test_grouped_gemm_binding_refusals():
                 dict(a_scale=torch.ones((1, 16))[:, ::2], b_scale=sb)):
         with pytest.raises(ValueError):
             fq.gemm(a, b, m_offsets=offs, **bad)
+    for bad in (torch.zeros((8, 128)), torch.zeros((7, 128), dtype=torch.bfloat16),
+                torch.zeros((128, 8), dtype=torch.bfloat16).t()):
+        with pytest.raises(ValueError):
+            fq.gemm(a, b, m_offsets=offs, a_scale=sa, b_scale=sb, out=bad)
     with pytest.raises(ValueError):                                          # wgrad: scales of too few chunks
         fq.gemm(torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((16, 256), dtype=torch.uint8),
                 layout=fq.FP8Q_WGRAD, a_scale=torch.ones((1, 8)), b_scale=torch.ones((2, 16)), m_offsets=offs)
