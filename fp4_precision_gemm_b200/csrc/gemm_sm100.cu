@@ -561,9 +561,9 @@ struct BwSmem {
   static constexpr uint32_t ring = b + stages * C::BStage;
   // epilogue staging per promotion warp: 32 rows x epi_cols BF16 or half as many FP32.  Grouped
   // GEMMs stage rows of 128 bytes, in the place of a fifth A/B stage: their K is short, so tiles
-  // end often, and the copy engine moves 128-byte rows in half the requests of 64-byte ones
-  // 32 experts, K 2048, N 7168, 65536 rows: 1314 -> 1263 us back to back; weight gradients of
-  // 32 x 2048 x 7168 into FP32: 1137 -> 1060 us; two or three buffers of 64-byte rows: no gain.
+  // end often, and the copy engine moves 128-byte rows in half the requests of 64-byte ones (32
+  // experts, K 2048, N 7168, 65536 rows: 1314 -> 1263 us back to back; weight gradients of 32 x
+  // 2048 x 7168 into FP32: 1137 -> 1060 us; two or three buffers of 64-byte rows: no gain).
   static constexpr int epi_cols = GROUPED ? 64 : 32;
   static constexpr uint32_t stage_c = 32 * epi_cols * 2;
   // staging buffers 1024-byte aligned: the TMA store's swizzle follows address bits
