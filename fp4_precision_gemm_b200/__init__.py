@@ -223,6 +223,10 @@ def _on(device, stream):
     return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -560,63 +564,68 @@ def quantize_nvfp4_2d16(w, rowwise=True, colwise=True, sf_layout=FP8Q_SF_MMA_TIL
     return out
 
 
+def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out, accumulate_fp32):
+    """Checks the tensors of a grouped gemm() (the kernels read whole tiles at the strides they are given: a wrong
+    shape would read past its tensor); returns the number of experts and C's shape."""
+    _check_offsets(m_offsets, a.device)
+    index = a.get_device()
+    for t in (b, a_scale, b_scale, out):
+        if t is not None and t.get_device() != index:
+            raise ValueError("grouped operands must be on one device")
+    groups, k_groups = m_offsets.numel() - 1, layout == FP8Q_WGRAD        # WGRAD: experts split K; C is stacked
+    if b.dim() != (2 if k_groups else 3) or a.dim() != 2:
+        raise ValueError("grouped b must be (G, N, K) codes, or (N, P) on the padded token axis for WGRAD")
+    if a.dtype is not torch.uint8 or b.dtype is not torch.uint8 or a.stride(1) != 1 or b.stride(-1) != 1:
+        raise ValueError("grouped a and b must be row-major uint8 codes")
+    (M, K), N = a.shape, b.shape[-2]
+    if b.shape[-1] != K:
+        raise ValueError("a and b must have the same K")
+    if not k_groups and (b.shape[0] != groups or b.stride(0) != N * b.stride(1)):
+        raise ValueError("b must hold one matrix per expert, one directly after the other")
+    kb, nb = K // 128, -(-N // 128)
+    if (a_scale is not None and ld_sa is None
+            and (a_scale.dim() != 2 or a_scale.shape[0] < kb or a_scale.shape[1] < M
+                 or a_scale.dtype is not torch.float32 or not a_scale.is_contiguous())):
+        raise ValueError("a_scale must be contiguous float32, (K/128, M or more)")
+    if b_scale is not None and ld_sb is None:
+        if b_scale.dtype is not torch.float32 or not b_scale.is_contiguous():
+            raise ValueError("b_scale must be contiguous float32")
+        if k_groups:
+            if b_scale.dim() != 2 or b_scale.shape[0] < kb or b_scale.shape[1] < N:
+                raise ValueError("b_scale must be (K/128, N or more)")
+        elif b_scale.shape != ((groups, kb, nb) if layout == FP8Q_DGRAD else (groups, nb, kb)):
+            raise ValueError("b_scale must be (G, N/128, K/128), or (G, K/128, N/128) for DGRAD")
+    shape = (groups, M, N) if k_groups else (M, N)
+    if out is not None:
+        if (out.dtype is not (torch.float32 if accumulate_fp32 else torch.bfloat16) or out.shape != shape
+                or out.stride(-1) != 1):
+            raise ValueError(f"grouped `out` must be row-major {shape}, bfloat16 or, with accumulate_fp32, float32")
+        if k_groups and out.stride(0) != M * out.stride(1):
+            raise ValueError("grouped WGRAD `out` must hold one matrix directly after the other")
+    if index < 0:
+        raise ValueError("grouped operands must be on a CUDA device")
+    return groups, shape
+
+
 def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets, out,
                accumulate_fp32, a_format, b_format, q_out, s_out):
     """The C ABI's argument block for gemm() (and the output tensor it writes)."""
-    M = a.shape[0]
-    grouped = m_offsets is not None
-    if grouped:
-        _check_offsets(m_offsets, a.device)
-    k_groups = grouped and layout == FP8Q_WGRAD        # experts split K; C is stacked
-    groups = m_offsets.numel() - 1 if grouped else 0
-    if grouped and any(t is not None and t.device != m_offsets.device for t in (b, a_scale, b_scale, out)):
-        raise ValueError("grouped operands must be on one device")
-    if grouped and b.dim() != (2 if k_groups else 3):
-        raise ValueError("grouped b must be (G, N, K) codes, or (N, P) on the padded token axis for WGRAD")
-    if grouped and not k_groups and (b.shape[0] != groups or b.stride(0) != b.shape[1] * b.stride(1)):
-        raise ValueError("b must hold one matrix per expert, one directly after the other")
-    N = b.shape[-2]
-    if grouped and recipe == FP8Q_BLOCKWISE:
-        # the kernels read whole tiles of scales at these strides: a wrong shape would read past them
-        kb, nb, rows = a.shape[1] // 128, -(-N // 128), M
-        want = (kb, N) if k_groups else (groups, kb, nb) if layout == FP8Q_DGRAD else (groups, nb, kb)
-        if a.shape[1] != b.shape[-1]:
-            raise ValueError("a and b must have the same K")
-        if (a_scale is not None and ld_sa is None
-                and (a_scale.dim() != 2 or a_scale.shape[0] < kb or a_scale.shape[1] < rows
-                     or not a_scale.is_contiguous())):
-            raise ValueError("a_scale must be contiguous, (K/128, M or more)")
-        if (b_scale is not None and ld_sb is None
-                and (b_scale.dim() != len(want) or not b_scale.is_contiguous()
-                     or (b_scale.shape[0] < kb or b_scale.shape[1] < N if k_groups else tuple(b_scale.shape) != want))):
-            raise ValueError(f"b_scale must be contiguous, {want}" + (" or more" if k_groups else ""))
-    if K is None:
-        K = a.shape[1] * (2 if recipe == FP8Q_NVFP4 else 1)
+    M, N = a.shape[0], b.shape[-2]
     if accumulate_fp32 and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate_fp32 needs an FP32 `out` tensor to update")
-    shape = (groups, M, N) if k_groups else (M, N)
-    c = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=a.device)
-    if grouped and (c.dtype != (torch.float32 if accumulate_fp32 else torch.bfloat16) or tuple(c.shape) != shape
-                    or c.stride(-1) != 1):
-        raise ValueError(f"grouped `out` must be row-major {shape}, bfloat16 or, with accumulate_fp32, float32")
-    if k_groups and c.stride(0) != M * c.stride(1):
-        raise ValueError("grouped WGRAD `out` must hold one matrix directly after the other")
-    args = GemmArgs()
-    args.recipe, args.layout = recipe, layout
-    args.M, args.N, args.K = M, N, K
-    args.a, args.lda = a.data_ptr(), a.stride(0)
-    args.b, args.ldb = b.data_ptr(), b.stride(-2)
-    args.a_scale = a_scale.data_ptr() if a_scale is not None else None
-    args.b_scale = b_scale.data_ptr() if b_scale is not None else None
-    args.ld_sa = ld_sa if ld_sa is not None else (a_scale.shape[-1] if (a_scale is not None and a_scale.dim() == 2) else 0)
-    args.ld_sb = ld_sb if ld_sb is not None else (b_scale.shape[-1] if (b_scale is not None and b_scale.dim() >= 2) else 0)
-    args.a_global = a_global.data_ptr() if a_global is not None else None
-    args.b_global = b_global.data_ptr() if b_global is not None else None
-    args.c, args.ldc = c.data_ptr(), c.stride(-2)
-    args.m_offsets = m_offsets.data_ptr() if grouped else None
-    args.num_groups = groups
-    args.c_fp32_accumulate = 1 if accumulate_fp32 else 0
-    args.a_format, args.b_format = a_format, b_format
+    groups, shape = 0, (M, N)
+    if m_offsets is not None:
+        groups, shape = _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out, accumulate_fp32)
+    if K is None:
+        K = a.shape[1] * (2 if recipe == FP8Q_NVFP4 else 1)
+    c = out if out is not None else a.new_empty(shape, dtype=torch.bfloat16)
+    if ld_sa is None:
+        ld_sa = a_scale.shape[-1] if (a_scale is not None and a_scale.dim() == 2) else 0
+    if ld_sb is None:
+        ld_sb = b_scale.shape[-1] if (b_scale is not None and b_scale.dim() >= 2) else 0
+    args = GemmArgs(recipe, layout, M, N, K, a.data_ptr(), _addr(a_scale), a.stride(0), ld_sa, b.data_ptr(),
+                    _addr(b_scale), b.stride(-2), ld_sb, _addr(a_global), _addr(b_global), c.data_ptr(), c.stride(-2),
+                    _addr(m_offsets), groups, 1 if accumulate_fp32 else 0, a_format, b_format)
     if q_out is not None or s_out is not None:
         args.q_out = q_out.data_ptr() if q_out is not None else None
         args.s_out = s_out.data_ptr() if s_out is not None else None
@@ -730,10 +739,6 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
     with _on(dev, stream):
         _check(fp8q_norm_residual(a, _stream(stream)), "fp8q_norm_residual")
     return o
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post=None, gate=None, alpha=1.0,

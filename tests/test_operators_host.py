@@ -81,34 +81,43 @@ def test_grouped_product_refusals():
 
 
 def test_grouped_gemm_binding_refusals():
-    """Shapes that the binding can see to be wrong."""
+    """Shapes that the binding can see to be wrong; everything right but the device is refused last."""
     a, b = torch.zeros((8, 128), dtype=torch.uint8), torch.zeros((2, 128, 128), dtype=torch.uint8)
     offs = torch.tensor([0, 4, 8], dtype=torch.int32)
-    with pytest.raises(ValueError):
-        fq.gemm(a, b, m_offsets=offs.long())
-    with pytest.raises(ValueError):
-        fq.gemm(a, b[0], m_offsets=offs)                                     # one matrix for two experts
-    with pytest.raises(ValueError):
-        fq.gemm(a, b[:1], m_offsets=offs)
-    with pytest.raises(ValueError):
-        fq.gemm(a, b, layout=fq.FP8Q_WGRAD, m_offsets=offs)                  # wgrad: b is 2-D
-    with pytest.raises(ValueError):
-        fq.gemm(a, b[0], layout=fq.FP8Q_WGRAD, m_offsets=offs, out=torch.zeros((2, 8, 64)), accumulate_fp32=True)
-    with pytest.raises(ValueError):
-        fq.gemm(a, b, m_offsets=offs[::2])
     sa, sb = torch.ones((1, 8)), torch.ones((2, 1, 1))
-    for bad in (dict(a_scale=torch.ones((1, 4)), b_scale=sb), dict(a_scale=torch.ones(8), b_scale=sb),
-                dict(a_scale=sa, b_scale=torch.ones((1, 1, 1))), dict(a_scale=sa, b_scale=torch.ones((2, 1, 2))),
-                dict(a_scale=torch.ones((1, 16))[:, ::2], b_scale=sb)):
-        with pytest.raises(ValueError):
-            fq.gemm(a, b, m_offsets=offs, **bad)
-    for bad in (torch.zeros((8, 128)), torch.zeros((7, 128), dtype=torch.bfloat16),
-                torch.zeros((128, 8), dtype=torch.bfloat16).t()):
-        with pytest.raises(ValueError):
-            fq.gemm(a, b, m_offsets=offs, a_scale=sa, b_scale=sb, out=bad)
-    with pytest.raises(ValueError):                                          # wgrad: scales of too few chunks
-        fq.gemm(torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((16, 256), dtype=torch.uint8),
-                layout=fq.FP8Q_WGRAD, a_scale=torch.ones((1, 8)), b_scale=torch.ones((2, 16)), m_offsets=offs)
+    bf16 = torch.bfloat16
+
+    def refused(why, a=a, b=b, m_offsets=offs, a_scale=sa, b_scale=sb, **kw):
+        with pytest.raises(ValueError, match=why):
+            fq.gemm(a, b, m_offsets=m_offsets, a_scale=a_scale, b_scale=b_scale, **kw)
+
+    refused("CUDA device")
+    refused("CUDA device", layout=fq.FP8Q_DGRAD, out=torch.zeros((8, 128), dtype=bf16))
+    refused("m_offsets", m_offsets=offs.long())
+    refused("m_offsets", m_offsets=offs[::2])
+    refused("m_offsets", m_offsets=offs[:1])
+    refused("must be .G, N, K.", b=b[0])                                     # one matrix for two experts
+    refused("one matrix per expert", b=b[:1])
+    refused("one matrix per expert", b=torch.zeros((4, 128, 128), dtype=torch.uint8)[::2])
+    refused("uint8", a=torch.zeros((8, 128)))
+    refused("uint8", a=torch.zeros((128, 8), dtype=torch.uint8).t())
+    refused("same K", a=torch.zeros((8, 256), dtype=torch.uint8), a_scale=torch.ones((2, 8)))
+    for bad in (torch.ones((1, 4)), torch.ones(8), torch.ones((1, 16))[:, ::2], sa.double()):
+        refused("a_scale", a_scale=bad)
+    for bad in (torch.ones((1, 1, 1)), torch.ones((2, 1, 2)), torch.ones((2, 1)), sb.bfloat16()):
+        refused("b_scale", b_scale=bad)
+    for bad in (torch.zeros((8, 128)), torch.zeros((7, 128), dtype=bf16), torch.zeros((128, 8), dtype=bf16).t()):
+        refused("`out`", out=bad)
+    refused("FP32 `out`", accumulate_fp32=True)
+    # wgrad: 2-D operands, scales of every chunk, a stacked result
+    w = dict(a=torch.zeros((8, 256), dtype=torch.uint8), b=torch.zeros((16, 256), dtype=torch.uint8),
+             layout=fq.FP8Q_WGRAD, a_scale=torch.ones((2, 8)), b_scale=torch.ones((2, 16)))
+    refused("CUDA device", **w)
+    refused("padded token axis", layout=fq.FP8Q_WGRAD)
+    refused("a_scale", **{**w, "a_scale": torch.ones((1, 8))})
+    refused("b_scale", **{**w, "b_scale": torch.ones((1, 16))})
+    refused("`out`", **w, out=torch.zeros((2, 8, 64)), accumulate_fp32=True)
+    refused("`out`", **w, out=torch.zeros((4, 8, 16))[::2], accumulate_fp32=True)
 
 
 def items(*rows):
