@@ -217,10 +217,15 @@ _HERE = contextlib.nullcontext()
 
 
 def _on(device, stream):
-    """Makes `device` current for a call on its tensors (and refuses a stream of another device)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    """Makes `device`, and `stream` if one is given, current for a call's allocations and launches: memory taken
+    for another stream than the one that writes it may still be in use there.  Refuses a stream of another
+    device."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    index = device.index                                   # None: host tensors, which the checks refuse
+    return _HERE if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _addr(t):
@@ -460,17 +465,15 @@ def quantize_1x128_grouped(x, m_offsets, rowwise=False, colwise=True, stream=Non
     R, C = x.shape
     groups = m_offsets.numel() - 1
     P = fp8q_grouped_capacity(R, groups)
-    dev = x.device
-    out = {"q_col": x.new_empty((C, P), dtype=torch.uint8),
-           "s_col": x.new_empty((P // 128, C + (-C) % 4), dtype=torch.float32)}
-    if rowwise:
-        out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
-        out["s_row"] = x.new_empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32)
-    with _on(dev, stream):
+    with _on(x.device, stream):
+        out = {"q_col": x.new_empty((C, P), dtype=torch.uint8),
+               "s_col": x.new_empty((P // 128, C + (-C) % 4), dtype=torch.float32)}
+        if rowwise:
+            out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
+            out["s_row"] = x.new_empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32)
         st = fp8q_quantize_1x128_grouped(_ptr(x), R, C, x.stride(0), _ptr(m_offsets), groups, _ptr(out.get("q_row")),
                                          _ptr(out.get("s_row")), out["s_row"].shape[1] if rowwise else 0,
-                                         _ptr(out["q_col"]), _ptr(out["s_col"]), out["s_col"].shape[1],
-                                         _stream(stream))
+                                         _ptr(out["q_col"]), _ptr(out["s_col"]), out["s_col"].shape[1], _stream())
     _check(st, "fp8q_quantize_1x128_grouped")
     return out
 
@@ -649,12 +652,14 @@ def gemm(a, b, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, a_scale=None, b_scale=N
     split_tail (BLOCKWISE, not grouped, no q_out): give the call the workspace it asks for
     (fp8q_gemm_workspace_bytes), taken from torch's caching allocator on the call's stream, so
     that a mostly idle last wave is split into K ranges."""
-    args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
-                         out, accumulate_fp32, a_format, b_format, q_out, s_out)
     if m_offsets is not None:
         with _on(a.device, stream):
-            _check(fp8q_gemm_blockscaled(args, _stream(stream)), "fp8q_gemm_blockscaled")
+            args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K,
+                                 m_offsets, out, accumulate_fp32, a_format, b_format, q_out, s_out)
+            _check(fp8q_gemm_blockscaled(args, _stream()), "fp8q_gemm_blockscaled")
         return c
+    args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
+                         out, accumulate_fp32, a_format, b_format, q_out, s_out)
     ws = None
     if split_tail and recipe == FP8Q_BLOCKWISE:
         nbytes = fp8q_gemm_workspace_bytes(args)
@@ -718,26 +723,26 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
     p_pre = _vector(w_pre, wd, C, index)
     p_post = None if w_post is None else _vector(w_post, wd, C, index)
     p_gate = None if gate is None else _vector(gate, wd, C, index)
-    if out is None:
-        out, ld_out = torch.empty_like(h, memory_format=torch.contiguous_format), C
-    else:
-        ld_out = _matrix(out, hd, shape, index)
-    rstd = y.new_empty((R,), dtype=torch.float32)
-    rstd_post = None if w_post is None else y.new_empty((R,), dtype=torch.float32)
-    o = {"h": out, "rstd_pre": rstd, "rstd_post": rstd_post}
-    n = q = sc = None
-    ld_s = 0
-    if normed:
-        o["n"] = n = torch.empty_like(y, memory_format=torch.contiguous_format)
-    if quantize:
-        ld_s = max(R, 1) + (-max(R, 1)) % 4
-        o["q_row"] = q = torch.empty_like(y, dtype=torch.uint8, memory_format=torch.contiguous_format)
-        o["s_row"] = sc = y.new_empty((C // 128, ld_s), dtype=torch.float32)
-    a = NormArgs(R, C, _DTYPES[hd], _DTYPES[wd], alpha, eps, y.data_ptr(), ld_y, h.data_ptr(), ld_h, p_post, p_gate,
-                 p_pre, out.data_ptr(), ld_out, _addr(n), C, _addr(q), _addr(sc), ld_s, _addr(rstd_post),
-                 rstd.data_ptr())
     with _on(dev, stream):
-        _check(fp8q_norm_residual(a, _stream(stream)), "fp8q_norm_residual")
+        if out is None:
+            out, ld_out = torch.empty_like(h, memory_format=torch.contiguous_format), C
+        else:
+            ld_out = _matrix(out, hd, shape, index)
+        rstd = y.new_empty((R,), dtype=torch.float32)
+        rstd_post = None if w_post is None else y.new_empty((R,), dtype=torch.float32)
+        o = {"h": out, "rstd_pre": rstd, "rstd_post": rstd_post}
+        n = q = sc = None
+        ld_s = 0
+        if normed:
+            o["n"] = n = torch.empty_like(y, memory_format=torch.contiguous_format)
+        if quantize:
+            ld_s = max(R, 1) + (-max(R, 1)) % 4
+            o["q_row"] = q = torch.empty_like(y, dtype=torch.uint8, memory_format=torch.contiguous_format)
+            o["s_row"] = sc = y.new_empty((C // 128, ld_s), dtype=torch.float32)
+        a = NormArgs(R, C, _DTYPES[hd], _DTYPES[wd], alpha, eps, y.data_ptr(), ld_y, h.data_ptr(), ld_h, p_post, p_gate,
+                     p_pre, out.data_ptr(), ld_out, _addr(n), C, _addr(q), _addr(sc), ld_s, _addr(rstd_post),
+                     rstd.data_ptr())
+        _check(fp8q_norm_residual(a, _stream()), "fp8q_norm_residual")
     return o
 
 
@@ -764,21 +769,19 @@ def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post
     if gate is not None:
         p_gate = _vector(gate, wd, C, index)
         names.append("dgate")
-    dh_in = torch.empty_like(h, memory_format=torch.contiguous_format)
-    dy = torch.empty_like(y, memory_format=torch.contiguous_format)
-    sums = y.new_empty((len(names), C), dtype=torch.float32)      # one allocation for the vectors
-    o = {"dh": dh_in, "dy": dy, **dict(zip(names, sums.unbind(0)))}
-    at = dict(zip(names, range(sums.data_ptr(), sums.data_ptr() + 4 * C * len(names), 4 * C)))
     with _on(dev, stream):
+        dh_in = torch.empty_like(h, memory_format=torch.contiguous_format)
+        dy = torch.empty_like(y, memory_format=torch.contiguous_format)
+        sums = y.new_empty((len(names), C), dtype=torch.float32)      # one allocation for the vectors
+        o = {"dh": dh_in, "dy": dy, **dict(zip(names, sums.unbind(0)))}
+        at = dict(zip(names, range(sums.data_ptr(), sums.data_ptr() + 4 * C * len(names), 4 * C)))
         nbytes = fp8q_norm_backward_workspace_bytes(R, C, _DTYPES[hd])
         ws = y.new_empty((max(nbytes, 16),), dtype=torch.uint8)
-        if stream is not None:
-            ws.record_stream(stream)
         a = NormBackwardArgs(R, C, _DTYPES[hd], _DTYPES[wd], alpha, dn.data_ptr(), ld_dn, dh.data_ptr(), ld_dh,
                              y.data_ptr(), ld_y, h.data_ptr(), ld_h, p_post, p_gate, p_pre, p_rstd_post, p_rstd,
                              dh_in.data_ptr(), C, dy.data_ptr(), C, at.get("dw_post"), at.get("dgate"), at["dw_pre"],
                              ws.data_ptr(), nbytes)
-        _check(fp8q_norm_residual_backward(a, _stream(stream)), "fp8q_norm_residual_backward")
+        _check(fp8q_norm_residual_backward(a, _stream()), "fp8q_norm_residual_backward")
     return o
 
 
@@ -808,14 +811,12 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
     words[1::4] = words[0::4] if out is None else [o.data_ptr() for o in outs]
     words[2::4], words[3::4] = sizes, [_DTYPES[k] for k in kinds]
     items = array.array("q", words)
-    nbytes = fp8q_clip_grad_workspace_bytes(len(grads))
-    ws = torch.empty(nbytes // 4 + 1, dtype=torch.float32, device=dev)     # the norm after the partial sums
-    norm, base = ws[nbytes // 4], ws.data_ptr()
-    if stream is not None:
-        ws.record_stream(stream)
+    nbytes = fp8q_clip_grad_workspace_bytes(n)
     with _on(dev, stream):
-        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps, ctypes.c_void_p(base + nbytes),
-                                 ctypes.c_void_p(base), nbytes, _stream(stream))
+        ws = torch.empty(nbytes // 4 + 1, dtype=torch.float32, device=dev)     # the norm after the partial sums
+        norm, base = ws[nbytes // 4], ws.data_ptr()
+        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps,
+                                 ctypes.c_void_p(base + nbytes), ctypes.c_void_p(base), nbytes, _stream())
     _check(st, "fp8q_clip_grad_norm")
     return norm
 

@@ -502,3 +502,40 @@ def test_two_host_threads(cuda_lib):
         th.join()
     for p, q in zip(alone, both):
         assert len(q) == 4 and all(torch.equal(u, v) for u, v in zip(p, q))
+
+
+def test_results_are_not_taken_from_memory_that_another_stream_still_uses(cuda_lib):
+    """Memory freed on the current stream, whose last kernel there has not run yet, is not handed to a call on
+    another stream: its late write would land in that call's result."""
+    fq = cuda_lib
+    a, b, sa, sb = codes((600, 256), 1), codes((2, 256, 256), 2), scales((2, 600), 3), scales((2, 2, 2), 4)
+    x = workloads.normal_bf16((600, 256), 1.0, 5, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    offs = offsets([300, 300])
+    side = torch.cuda.Stream()
+    calls = {
+        "gemm": lambda s: [fq.gemm(a, b, a_scale=sa, b_scale=sb, m_offsets=offs, stream=s)],
+        "quantize": lambda s: list(fq.quantize_1x128_grouped(x, offs, rowwise=True, stream=s).values()),
+        "norm": lambda s: list(fq.norm_residual(x, x, w, w, w, quantize=True, stream=s).values()),
+        "clip": lambda s: [fq.clip_grad_norm([x], 1.0, out=[y], stream=s)],
+    }
+    y = torch.empty_like(x)
+    r = fq.norm_residual(x, x, w, w, w)
+    calls["backward"] = lambda s: list(fq.norm_residual_backward(x, x, x, r["h"], r["rstd_pre"], w, w, r["rstd_post"],
+                                                                 w, stream=s).values())
+    for name, call in calls.items():
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        sizes = [t.untyped_storage().nbytes() for t in call(None)]
+        torch.cuda.synchronize()
+        old = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda._sleep(200_000_000)                       # about a tenth of a second
+        for t in old:
+            t.fill_(0x7F)
+        del old, t
+        got = call(side)
+        torch.cuda.synchronize()
+        for u, v in zip(want, got):
+            if name == "quantize" and u.dtype == torch.float32:
+                u, v = u[:, :256], v[:, :256]
+            assert torch.equal(u, v), name
