@@ -473,6 +473,8 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
 
 namespace {
 
+constexpr int kRingBytes = 220 * 1024;   // shared memory of an SM's rows; no launch takes more
+
 struct NormShape {
   int nv, threads, stages, smem, grid;
 };
@@ -486,15 +488,14 @@ struct NormShape {
 // would cost the large case 5%.  Up to 4 rows are staged per CTA, as many as its share of shared
 // memory takes.
 NormShape norm_shape(int64_t rows, int cols, int row_bytes, int num_sms, bool wide) {
-  constexpr int kSmem = 220 * 1024;
   NormShape s;
   const int vecs = (cols + 7) / 8;
   s.nv = wide ? 4 : vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
   s.threads = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
   int ctas = 512 / s.threads;
-  if (ctas > kSmem / (row_bytes + 1024)) ctas = kSmem / (row_bytes + 1024);
+  if (ctas > kRingBytes / (row_bytes + 1024)) ctas = kRingBytes / (row_bytes + 1024);
   if (ctas < 1) ctas = 1;
-  s.stages = (kSmem / ctas - 1024) / row_bytes;
+  s.stages = (kRingBytes / ctas - 1024) / row_bytes;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   if (s.stages < 1) s.stages = 1;
   s.smem = s.stages * row_bytes;
@@ -503,9 +504,11 @@ NormShape norm_shape(int64_t rows, int cols, int row_bytes, int num_sms, bool wi
   return s;
 }
 
+// The limit belongs to the kernel, which calls of other widths share: always the same value, so that another
+// thread's call between these two lines changes nothing.
 template <class K>
 cudaError_t launch_rows(K kern, const NormShape& s, const NormParams& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
   kern<<<s.grid, s.threads, s.smem, st>>>(p);
   return cudaGetLastError();
