@@ -567,9 +567,15 @@ def quantize_nvfp4_2d16(w, rowwise=True, colwise=True, sf_layout=FP8Q_SF_MMA_TIL
     return out
 
 
-def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out, accumulate_fp32):
+def _reaches(t, rows, cols, ld):
+    """Whether `rows` rows of `cols` elements, `ld` apart, lie within t (from its first element to its last)."""
+    span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
+    return ld >= cols and (rows == 0 or (rows - 1) * ld + cols <= span)
+
+
+def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, K, m_offsets, out, accumulate_fp32):
     """Checks the tensors of a grouped gemm() (the kernels read whole tiles at the strides they are given: a wrong
-    shape would read past its tensor); returns the number of experts and C's shape."""
+    shape would read past its tensor); returns the number of experts, K and C's shape."""
     _check_offsets(m_offsets, a.device)
     index = a.get_device()
     for t in (b, a_scale, b_scale, out):
@@ -580,16 +586,27 @@ def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out,
         raise ValueError("grouped b must be (G, N, K) codes, or (N, P) on the padded token axis for WGRAD")
     if a.dtype is not torch.uint8 or b.dtype is not torch.uint8 or a.stride(1) != 1 or b.stride(-1) != 1:
         raise ValueError("grouped a and b must be row-major uint8 codes")
-    (M, K), N = a.shape, b.shape[-2]
-    if b.shape[-1] != K:
-        raise ValueError("a and b must have the same K")
+    M, N = a.shape[0], b.shape[-2]
+    if K is None:
+        K = a.shape[1]
+        if b.shape[-1] != K:
+            raise ValueError("a and b must have the same K")
+    elif not 0 <= K <= min(a.shape[1], b.shape[-1]):
+        raise ValueError(f"K must be between 0 and the columns of a and b: {K}, {a.shape[1]}, {b.shape[-1]}")
     if not k_groups and (b.shape[0] != groups or b.stride(0) != N * b.stride(1)):
         raise ValueError("b must hold one matrix per expert, one directly after the other")
-    kb, nb = K // 128, -(-N // 128)
+    kb, nb = -(-K // 128), -(-N // 128)
     if (a_scale is not None and ld_sa is None
             and (a_scale.dim() != 2 or a_scale.shape[0] < kb or a_scale.shape[1] < M
                  or a_scale.dtype is not torch.float32 or not a_scale.is_contiguous())):
         raise ValueError("a_scale must be contiguous float32, (K/128, M or more)")
+    if a_scale is not None and ld_sa is not None and (a_scale.dtype is not torch.float32
+                                                      or not _reaches(a_scale, kb, M, ld_sa)):
+        raise ValueError("a_scale must be float32 and hold K/128 rows of M, ld_sa apart")
+    if b_scale is not None and ld_sb is not None:
+        rows, cols = (kb, N) if k_groups else (groups * kb, nb) if layout == FP8Q_DGRAD else (groups * nb, kb)
+        if b_scale.dtype is not torch.float32 or not _reaches(b_scale, rows, cols, ld_sb):
+            raise ValueError(f"b_scale must be float32 and hold {rows} rows of {cols}, ld_sb apart")
     if b_scale is not None and ld_sb is None:
         if b_scale.dtype is not torch.float32 or not b_scale.is_contiguous():
             raise ValueError("b_scale must be contiguous float32")
@@ -607,7 +624,7 @@ def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out,
             raise ValueError("grouped WGRAD `out` must hold one matrix directly after the other")
     if index < 0:
         raise ValueError("grouped operands must be on a CUDA device")
-    return groups, shape
+    return groups, K, shape
 
 
 def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets, out,
@@ -618,7 +635,8 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
         raise ValueError("accumulate_fp32 needs an FP32 `out` tensor to update")
     groups, shape = 0, (M, N)
     if m_offsets is not None:
-        groups, shape = _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, m_offsets, out, accumulate_fp32)
+        groups, K, shape = _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, K, m_offsets, out,
+                                          accumulate_fp32)
     if K is None:
         K = a.shape[1] * (2 if recipe == FP8Q_NVFP4 else 1)
     c = out if out is not None else a.new_empty(shape, dtype=torch.bfloat16)
