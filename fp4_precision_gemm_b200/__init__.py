@@ -228,6 +228,17 @@ def _on(device, stream):
     return _HERE if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
+def _results(stream, *made):
+    """Tensors that a call made on `stream` (None: the current one) are the caller's to use on the current stream:
+    their memory is not given to another call on `stream` before that use has ended."""
+    if stream is not None:
+        here = torch.cuda.current_stream(stream.device)
+        if here != stream:
+            for t in made:
+                if t is not None:
+                    t.record_stream(here)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -475,6 +486,7 @@ def quantize_1x128_grouped(x, m_offsets, rowwise=False, colwise=True, stream=Non
                                          _ptr(out.get("s_row")), out["s_row"].shape[1] if rowwise else 0,
                                          _ptr(out["q_col"]), _ptr(out["s_col"]), out["s_col"].shape[1], _stream())
     _check(st, "fp8q_quantize_1x128_grouped")
+    _results(stream, *out.values())
     return out
 
 
@@ -675,6 +687,7 @@ def gemm(a, b, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, a_scale=None, b_scale=N
             args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K,
                                  m_offsets, out, accumulate_fp32, a_format, b_format, q_out, s_out)
             _check(fp8q_gemm_blockscaled(args, _stream()), "fp8q_gemm_blockscaled")
+        _results(stream, c if out is None else None)
         return c
     args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
                          out, accumulate_fp32, a_format, b_format, q_out, s_out)
@@ -742,8 +755,10 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
     p_post = None if w_post is None else _vector(w_post, wd, C, index)
     p_gate = None if gate is None else _vector(gate, wd, C, index)
     with _on(dev, stream):
+        own = None
         if out is None:
-            out, ld_out = torch.empty_like(h, memory_format=torch.contiguous_format), C
+            own = out = torch.empty_like(h, memory_format=torch.contiguous_format)
+            ld_out = C
         else:
             ld_out = _matrix(out, hd, shape, index)
         rstd = y.new_empty((R,), dtype=torch.float32)
@@ -761,6 +776,7 @@ def norm_residual(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, norm
                      p_pre, out.data_ptr(), ld_out, _addr(n), C, _addr(q), _addr(sc), ld_s, _addr(rstd_post),
                      rstd.data_ptr())
         _check(fp8q_norm_residual(a, _stream()), "fp8q_norm_residual")
+    _results(stream, own, rstd, rstd_post, n, q, sc)
     return o
 
 
@@ -800,6 +816,7 @@ def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post
                              dh_in.data_ptr(), C, dy.data_ptr(), C, at.get("dw_post"), at.get("dgate"), at["dw_pre"],
                              ws.data_ptr(), nbytes)
         _check(fp8q_norm_residual_backward(a, _stream()), "fp8q_norm_residual_backward")
+    _results(stream, dh_in, dy, sums)
     return o
 
 
@@ -836,6 +853,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
         st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps,
                                  ctypes.c_void_p(base + nbytes), ctypes.c_void_p(base), nbytes, _stream())
     _check(st, "fp8q_clip_grad_norm")
+    _results(stream, norm)
     return norm
 
 
