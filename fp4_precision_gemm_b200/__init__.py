@@ -363,18 +363,19 @@ def quantize_1x128(x, rowwise=True, colwise=False, stream=None):
     q_col (C, R) uint8, s_col (R/128, C) float32."""
     _check_bf16(x)
     R, C = x.shape
-    out = {}
-    dev = x.device
-    if rowwise:
-        out["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-        out["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
-    if colwise:
-        out["q_col"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
-        out["s_col"] = torch.empty((R // 128, C + (-C) % 4), dtype=torch.float32, device=dev)
-    st = fp8q_quantize_1x128(_ptr(x), R, C, x.stride(0), _ptr(out.get("q_row")), _ptr(out.get("s_row")),
-                             out["s_row"].shape[1] if rowwise else 0, _ptr(out.get("q_col")),
-                             _ptr(out.get("s_col")), out["s_col"].shape[1] if colwise else 0, _stream(stream))
+    with _on(x.device, stream):
+        out = {}
+        if rowwise:
+            out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
+            out["s_row"] = x.new_empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32)
+        if colwise:
+            out["q_col"] = x.new_empty((C, R), dtype=torch.uint8)
+            out["s_col"] = x.new_empty((R // 128, C + (-C) % 4), dtype=torch.float32)
+        st = fp8q_quantize_1x128(_ptr(x), R, C, x.stride(0), _ptr(out.get("q_row")), _ptr(out.get("s_row")),
+                                 out["s_row"].shape[1] if rowwise else 0, _ptr(out.get("q_col")),
+                                 _ptr(out.get("s_col")), out["s_col"].shape[1] if colwise else 0, _stream())
     _check(st, "fp8q_quantize_1x128")
+    _results(stream, *out.values())
     return out
 
 
@@ -382,15 +383,16 @@ def quantize_128x128(w, transposed=True, plain=True, stream=None):
     """128x128 blocks of W (K x N).  Returns q_t (N, K), q (K, N), s (N/128, K/128)."""
     _check_bf16(w, "w")
     K, N = w.shape
-    dev = w.device
-    out = {"s": torch.empty((N // 128, K // 128), dtype=torch.float32, device=dev)}
-    if transposed:
-        out["q_t"] = torch.empty((N, K), dtype=torch.uint8, device=dev)
-    if plain:
-        out["q"] = torch.empty((K, N), dtype=torch.uint8, device=dev)
-    st = fp8q_quantize_128x128(_ptr(w), K, N, w.stride(0), _ptr(out.get("q_t")), _ptr(out.get("q")),
-                               _ptr(out["s"]), _stream(stream))
+    with _on(w.device, stream):
+        out = {"s": w.new_empty((N // 128, K // 128), dtype=torch.float32)}
+        if transposed:
+            out["q_t"] = w.new_empty((N, K), dtype=torch.uint8)
+        if plain:
+            out["q"] = w.new_empty((K, N), dtype=torch.uint8)
+        st = fp8q_quantize_128x128(_ptr(w), K, N, w.stride(0), _ptr(out.get("q_t")), _ptr(out.get("q")),
+                                   _ptr(out["s"]), _stream())
     _check(st, "fp8q_quantize_128x128")
+    _results(stream, *out.values())
     return out
 
 
@@ -398,43 +400,45 @@ def quantize_multi(specs, stream=None):
     """Several quantizations in one launch.  specs: a list of ("1x128", x, rowwise, colwise)
     and ("128x128", w, transposed, plain) tuples.  Returns one output dict per spec, laid
     out exactly as quantize_1x128 / quantize_128x128 return them."""
-    items = (QuantItem * max(len(specs), 1))()
-    outs = []
-    n = 0
-    for spec in specs:
-        kind, x, a, b = spec
-        _check_bf16(x)
-        R, C = x.shape
-        dev = x.device
-        it = items[n] if x.numel() else QuantItem()   # an empty tensor has nothing to launch
-        n += 1 if x.numel() else 0
-        it.x, it.rows, it.cols, it.ld_x = x.data_ptr(), R, C, x.stride(0)
-        out = {}
-        if kind == "1x128":
-            it.kind = FP8Q_ITEM_1X128
-            if a:
-                out["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-                out["s_row"] = torch.empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32, device=dev)
-                it.q_row, it.s_row, it.ld_s_row = out["q_row"].data_ptr(), out["s_row"].data_ptr(), out["s_row"].shape[1]
-            if b:
-                out["q_col"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
-                out["s_col"] = torch.empty((R // 128, C + (-C) % 4), dtype=torch.float32, device=dev)
-                it.q_col, it.s_col, it.ld_s_col = out["q_col"].data_ptr(), out["s_col"].data_ptr(), out["s_col"].shape[1]
-        elif kind == "128x128":
-            it.kind = FP8Q_ITEM_128X128
-            out["s"] = torch.empty((C // 128, R // 128), dtype=torch.float32, device=dev)
-            it.s = out["s"].data_ptr()
-            if a:
-                out["q_t"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
-                it.q_t = out["q_t"].data_ptr()
-            if b:
-                out["q"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-                it.q = out["q"].data_ptr()
-        else:
-            raise ValueError(f"unknown quantization kind {kind!r}")
-        outs.append(out)
-    st = fp8q_quantize_multi(items, n, _stream(stream))
+    with _on(specs[0][1].device, stream) if specs else _HERE:
+        items = (QuantItem * max(len(specs), 1))()
+        outs = []
+        n = 0
+        for spec in specs:
+            kind, x, a, b = spec
+            _check_bf16(x)
+            R, C = x.shape
+            it = items[n] if x.numel() else QuantItem()   # an empty tensor has nothing to launch
+            n += 1 if x.numel() else 0
+            it.x, it.rows, it.cols, it.ld_x = x.data_ptr(), R, C, x.stride(0)
+            out = {}
+            if kind == "1x128":
+                it.kind = FP8Q_ITEM_1X128
+                if a:
+                    out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
+                    out["s_row"] = x.new_empty((C // 128, max(R, 1) + (-max(R, 1)) % 4), dtype=torch.float32)
+                    it.q_row, it.s_row, it.ld_s_row = out["q_row"].data_ptr(), out["s_row"].data_ptr(), out["s_row"].shape[1]
+                if b:
+                    out["q_col"] = x.new_empty((C, R), dtype=torch.uint8)
+                    out["s_col"] = x.new_empty((R // 128, C + (-C) % 4), dtype=torch.float32)
+                    it.q_col, it.s_col, it.ld_s_col = out["q_col"].data_ptr(), out["s_col"].data_ptr(), out["s_col"].shape[1]
+            elif kind == "128x128":
+                it.kind = FP8Q_ITEM_128X128
+                out["s"] = x.new_empty((C // 128, R // 128), dtype=torch.float32)
+                it.s = out["s"].data_ptr()
+                if a:
+                    out["q_t"] = x.new_empty((C, R), dtype=torch.uint8)
+                    it.q_t = out["q_t"].data_ptr()
+                if b:
+                    out["q"] = x.new_empty((R, C), dtype=torch.uint8)
+                    it.q = out["q"].data_ptr()
+            else:
+                raise ValueError(f"unknown quantization kind {kind!r}")
+            outs.append(out)
+        st = fp8q_quantize_multi(items, n, _stream())
     _check(st, "fp8q_quantize_multi")
+    for out in outs:
+        _results(stream, *out.values())
     return outs
 
 
@@ -446,15 +450,16 @@ def quantize_128x128_grouped(w, transposed=True, plain=True, stream=None):
     if w.stride(2) != 1 or w.stride(0) != w.shape[1] * w.stride(1):
         raise ValueError("w must hold contiguous row-major matrices (row stride may be padded)")
     G, K, N = w.shape
-    dev = w.device
-    out = {"s": torch.empty((G, N // 128, K // 128), dtype=torch.float32, device=dev)}
-    if transposed:
-        out["q_t"] = torch.empty((G, N, K), dtype=torch.uint8, device=dev)
-    if plain:
-        out["q"] = torch.empty((G, K, N), dtype=torch.uint8, device=dev)
-    st = fp8q_quantize_128x128_grouped(_ptr(w), G, K, N, w.stride(1), _ptr(out.get("q_t")), _ptr(out.get("q")),
-                                       _ptr(out["s"]), _stream(stream))
+    with _on(w.device, stream):
+        out = {"s": w.new_empty((G, N // 128, K // 128), dtype=torch.float32)}
+        if transposed:
+            out["q_t"] = w.new_empty((G, N, K), dtype=torch.uint8)
+        if plain:
+            out["q"] = w.new_empty((G, K, N), dtype=torch.uint8)
+        st = fp8q_quantize_128x128_grouped(_ptr(w), G, K, N, w.stride(1), _ptr(out.get("q_t")), _ptr(out.get("q")),
+                                           _ptr(out["s"]), _stream())
     _check(st, "fp8q_quantize_128x128_grouped")
+    _results(stream, *out.values())
     return out
 
 
@@ -495,17 +500,18 @@ def quantize_mx32(x, rowwise=True, colwise=False, sf_layout=FP8Q_SF_ROWMAJOR, st
     buffers sized by fp8q_sf_bytes for the chosen layout)."""
     _check_bf16(x)
     R, C = x.shape
-    dev = x.device
-    out = {}
-    if rowwise:
-        out["q_row"] = torch.empty((R, C), dtype=torch.uint8, device=dev)
-        out["e8m0_row"] = torch.empty(fp8q_sf_bytes(FP8Q_MXFP8, R, C, sf_layout), dtype=torch.uint8, device=dev)
-    if colwise:
-        out["q_col"] = torch.empty((C, R), dtype=torch.uint8, device=dev)
-        out["e8m0_col"] = torch.empty(fp8q_sf_bytes(FP8Q_MXFP8, C, R, sf_layout), dtype=torch.uint8, device=dev)
-    st = fp8q_quantize_mx32(_ptr(x), R, C, x.stride(0), _ptr(out.get("q_row")), _ptr(out.get("e8m0_row")),
-                            _ptr(out.get("q_col")), _ptr(out.get("e8m0_col")), sf_layout, _stream(stream))
+    with _on(x.device, stream):
+        out = {}
+        if rowwise:
+            out["q_row"] = x.new_empty((R, C), dtype=torch.uint8)
+            out["e8m0_row"] = x.new_empty(fp8q_sf_bytes(FP8Q_MXFP8, R, C, sf_layout), dtype=torch.uint8)
+        if colwise:
+            out["q_col"] = x.new_empty((C, R), dtype=torch.uint8)
+            out["e8m0_col"] = x.new_empty(fp8q_sf_bytes(FP8Q_MXFP8, C, R, sf_layout), dtype=torch.uint8)
+        st = fp8q_quantize_mx32(_ptr(x), R, C, x.stride(0), _ptr(out.get("q_row")), _ptr(out.get("e8m0_row")),
+                                _ptr(out.get("q_col")), _ptr(out.get("e8m0_col")), sf_layout, _stream())
     _check(st, "fp8q_quantize_mx32")
+    _results(stream, *out.values())
     return out
 
 
@@ -513,10 +519,12 @@ def quantize_tensor(x, stream=None):
     """Per-tensor current scaling.  Returns q (R, C) uint8 and s_dec (1,) float32."""
     _check_bf16(x)
     R, C = x.shape
-    out = {"q": torch.empty((R, C), dtype=torch.uint8, device=x.device),
-           "s_dec": torch.empty((1,), dtype=torch.float32, device=x.device)}
-    st = fp8q_quantize_tensor(_ptr(x), R, C, x.stride(0), _ptr(out["q"]), _ptr(out["s_dec"]), _stream(stream))
+    with _on(x.device, stream):
+        out = {"q": x.new_empty((R, C), dtype=torch.uint8),
+               "s_dec": x.new_empty((1,), dtype=torch.float32)}
+        st = fp8q_quantize_tensor(_ptr(x), R, C, x.stride(0), _ptr(out["q"]), _ptr(out["s_dec"]), _stream())
     _check(st, "fp8q_quantize_tensor")
+    _results(stream, *out.values())
     return out
 
 
@@ -527,11 +535,13 @@ def quantize_tensor_delayed(x, amax_history, history_pos, fmt=FP8Q_E4M3, stream=
     if not (amax_history.is_cuda and amax_history.dtype == torch.float32 and amax_history.dim() == 1):
         raise ValueError("amax_history must be a 1-D float32 CUDA tensor")
     R, C = x.shape
-    out = {"q": torch.empty((R, C), dtype=torch.uint8, device=x.device),
-           "s_dec": torch.empty((1,), dtype=torch.float32, device=x.device)}
-    st = fp8q_quantize_tensor_delayed(_ptr(x), R, C, x.stride(0), _ptr(amax_history), amax_history.numel(),
-                                      history_pos, fmt, _ptr(out["q"]), _ptr(out["s_dec"]), _stream(stream))
+    with _on(x.device, stream):
+        out = {"q": x.new_empty((R, C), dtype=torch.uint8),
+               "s_dec": x.new_empty((1,), dtype=torch.float32)}
+        st = fp8q_quantize_tensor_delayed(_ptr(x), R, C, x.stride(0), _ptr(amax_history), amax_history.numel(),
+                                          history_pos, fmt, _ptr(out["q"]), _ptr(out["s_dec"]), _stream())
     _check(st, "fp8q_quantize_tensor_delayed")
+    _results(stream, *out.values())
     return out
 
 
@@ -541,21 +551,22 @@ def rht16_quantize_sr(x, rowwise=True, colwise=False, rht=0, rht_seed=0, sr=0, s
     g_row (1,) and/or q_col (C, R/2), sf_col, g_col (1,)."""
     _check_bf16(x)
     R, C = x.shape
-    dev = x.device
-    out = {}
-    if rowwise:
-        out["q_row"] = torch.empty((R, C // 2), dtype=torch.uint8, device=dev)
-        out["sf_row"] = torch.empty(fp8q_sf_bytes(FP8Q_NVFP4, R, C, sf_layout), dtype=torch.uint8, device=dev)
-        out["g_row"] = torch.empty((1,), dtype=torch.float32, device=dev)
-    if colwise:
-        out["q_col"] = torch.empty((C, R // 2), dtype=torch.uint8, device=dev)
-        out["sf_col"] = torch.empty(fp8q_sf_bytes(FP8Q_NVFP4, C, R, sf_layout), dtype=torch.uint8, device=dev)
-        out["g_col"] = torch.empty((1,), dtype=torch.float32, device=dev)
-    st = fp4q_rht16_quantize_sr(_ptr(x), R, C, x.stride(0), rht, rht_seed, sr, sr_seed,
-                                _ptr(out.get("q_row")), _ptr(out.get("sf_row")), _ptr(out.get("g_row")),
-                                _ptr(out.get("q_col")), _ptr(out.get("sf_col")), _ptr(out.get("g_col")),
-                                sf_layout, _stream(stream))
+    with _on(x.device, stream):
+        out = {}
+        if rowwise:
+            out["q_row"] = x.new_empty((R, C // 2), dtype=torch.uint8)
+            out["sf_row"] = x.new_empty(fp8q_sf_bytes(FP8Q_NVFP4, R, C, sf_layout), dtype=torch.uint8)
+            out["g_row"] = x.new_empty((1,), dtype=torch.float32)
+        if colwise:
+            out["q_col"] = x.new_empty((C, R // 2), dtype=torch.uint8)
+            out["sf_col"] = x.new_empty(fp8q_sf_bytes(FP8Q_NVFP4, C, R, sf_layout), dtype=torch.uint8)
+            out["g_col"] = x.new_empty((1,), dtype=torch.float32)
+        st = fp4q_rht16_quantize_sr(_ptr(x), R, C, x.stride(0), rht, rht_seed, sr, sr_seed,
+                                    _ptr(out.get("q_row")), _ptr(out.get("sf_row")), _ptr(out.get("g_row")),
+                                    _ptr(out.get("q_col")), _ptr(out.get("sf_col")), _ptr(out.get("g_col")),
+                                    sf_layout, _stream())
     _check(st, "fp4q_rht16_quantize_sr")
+    _results(stream, *out.values())
     return out
 
 
@@ -564,18 +575,19 @@ def quantize_nvfp4_2d16(w, rowwise=True, colwise=True, sf_layout=FP8Q_SF_MMA_TIL
     q_col (C, R/2), sf_col, and g (1,), the decode scale both layouts share."""
     _check_bf16(w, "w")
     R, C = w.shape
-    dev = w.device
-    out = {"g": torch.empty((1,), dtype=torch.float32, device=dev)}
-    if rowwise:
-        out["q_row"] = torch.empty((R, C // 2), dtype=torch.uint8, device=dev)
-        out["sf_row"] = torch.empty(fp8q_sf_bytes(FP8Q_NVFP4, R, C, sf_layout), dtype=torch.uint8, device=dev)
-    if colwise:
-        out["q_col"] = torch.empty((C, R // 2), dtype=torch.uint8, device=dev)
-        out["sf_col"] = torch.empty(fp8q_sf_bytes(FP8Q_NVFP4, C, R, sf_layout), dtype=torch.uint8, device=dev)
-    st = fp4q_quantize_2d16(_ptr(w), R, C, w.stride(0), _ptr(out.get("q_row")), _ptr(out.get("sf_row")),
-                            _ptr(out.get("q_col")), _ptr(out.get("sf_col")), _ptr(out["g"]), sf_layout,
-                            _stream(stream))
+    with _on(w.device, stream):
+        out = {"g": w.new_empty((1,), dtype=torch.float32)}
+        if rowwise:
+            out["q_row"] = w.new_empty((R, C // 2), dtype=torch.uint8)
+            out["sf_row"] = w.new_empty(fp8q_sf_bytes(FP8Q_NVFP4, R, C, sf_layout), dtype=torch.uint8)
+        if colwise:
+            out["q_col"] = w.new_empty((C, R // 2), dtype=torch.uint8)
+            out["sf_col"] = w.new_empty(fp8q_sf_bytes(FP8Q_NVFP4, C, R, sf_layout), dtype=torch.uint8)
+        st = fp4q_quantize_2d16(_ptr(w), R, C, w.stride(0), _ptr(out.get("q_row")), _ptr(out.get("sf_row")),
+                                _ptr(out.get("q_col")), _ptr(out.get("sf_col")), _ptr(out["g"]), sf_layout,
+                                _stream())
     _check(st, "fp4q_quantize_2d16")
+    _results(stream, *out.values())
     return out
 
 
@@ -682,24 +694,16 @@ def gemm(a, b, recipe=FP8Q_BLOCKWISE, layout=FP8Q_FPROP, a_scale=None, b_scale=N
     split_tail (BLOCKWISE, not grouped, no q_out): give the call the workspace it asks for
     (fp8q_gemm_workspace_bytes), taken from torch's caching allocator on the call's stream, so
     that a mostly idle last wave is split into K ranges."""
-    if m_offsets is not None:
-        with _on(a.device, stream):
-            args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K,
-                                 m_offsets, out, accumulate_fp32, a_format, b_format, q_out, s_out)
-            _check(fp8q_gemm_blockscaled(args, _stream()), "fp8q_gemm_blockscaled")
-        _results(stream, c if out is None else None)
-        return c
-    args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
-                         out, accumulate_fp32, a_format, b_format, q_out, s_out)
-    ws = None
-    if split_tail and recipe == FP8Q_BLOCKWISE:
-        nbytes = fp8q_gemm_workspace_bytes(args)
-        if nbytes > 0:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=a.device)
-            if stream is not None:
-                ws.record_stream(stream)
-            args.workspace, args.workspace_bytes = ws.data_ptr(), nbytes
-    _check(fp8q_gemm_blockscaled(args, _stream(stream)), "fp8q_gemm_blockscaled")
+    with _on(a.device, stream):
+        args, c = _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b_global, K, m_offsets,
+                             out, accumulate_fp32, a_format, b_format, q_out, s_out)
+        if split_tail and recipe == FP8Q_BLOCKWISE and m_offsets is None:
+            nbytes = fp8q_gemm_workspace_bytes(args)
+            if nbytes > 0:
+                ws = a.new_empty((nbytes,), dtype=torch.uint8)
+                args.workspace, args.workspace_bytes = ws.data_ptr(), nbytes
+        _check(fp8q_gemm_blockscaled(args, _stream()), "fp8q_gemm_blockscaled")
+    _results(stream, c if out is None else None)
     return c
 
 
