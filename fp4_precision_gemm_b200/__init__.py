@@ -464,9 +464,9 @@ def quantize_128x128_grouped(w, transposed=True, plain=True, stream=None):
 
 
 def _check_offsets(m_offsets, device):
-    if not (m_offsets.device == device and m_offsets.dtype == torch.int32 and m_offsets.dim() == 1
-            and m_offsets.is_contiguous() and m_offsets.numel() >= 2):
-        raise ValueError("m_offsets must be a contiguous 1-D int32 tensor of groups + 1 offsets on the operands' device")
+    if not (m_offsets.device == device and m_offsets.dtype == torch.int32 and m_offsets.is_contiguous()
+            and m_offsets.numel() >= 2):
+        raise ValueError("m_offsets must be a contiguous int32 tensor of groups + 1 offsets on the operands' device")
 
 
 def quantize_1x128_grouped(x, m_offsets, rowwise=False, colwise=True, stream=None):
@@ -591,63 +591,70 @@ def quantize_nvfp4_2d16(w, rowwise=True, colwise=True, sf_layout=FP8Q_SF_MMA_TIL
     return out
 
 
-def _reaches(t, rows, cols, ld):
-    """Whether `rows` rows of `cols` elements, `ld` apart, lie within t (from its first element to its last)."""
-    span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
-    return ld >= cols and (rows == 0 or (rows - 1) * ld + cols <= span)
+_CODES = (torch.uint8, torch.int8, torch.float8_e4m3fn)       # E4M3 codes, by any of their types
+
+
+def _check_scales(name, t, ld, rows, cols, experts=1):
+    """Checks that t holds `experts` times `rows` rows of `cols` scales, every row `ld` after the one before it; ld
+    None: t is contiguous and its last dimension is ld."""
+    if t is None:
+        return
+    shape, n = t.shape, experts * rows
+    if ld is not None:                                             # what t spans, from its first element to its last
+        span = 1 + sum((k - 1) * s for k, s in zip(shape, t.stride())) if t.numel() else 0
+    else:
+        ld, span = shape[-1] if len(shape) > 1 else 0, t.numel()
+        # experts in a dimension of their own must also be `rows` rows apart
+        if not t.is_contiguous() or (experts > 1 and len(shape) > 2 and shape[0] > 1 and span != shape[0] * rows * ld):
+            span = -1
+    if t.dtype is not torch.float32 or ld < cols or span < 0 or (n and (n - 1) * ld + cols > span):
+        raise ValueError(f"{name} must be float32 and hold {experts} x {rows} rows of {cols}: contiguous, or its "
+                         f"leading dimension given")
 
 
 def _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, K, m_offsets, out, accumulate_fp32):
     """Checks the tensors of a grouped gemm() (the kernels read whole tiles at the strides they are given: a wrong
-    shape would read past its tensor); returns the number of experts, K and C's shape."""
+    shape would read past its tensor) for what the kernels read and write of them; returns the number of experts,
+    K and C's shape."""
     _check_offsets(m_offsets, a.device)
     index = a.get_device()
     for t in (b, a_scale, b_scale, out):
         if t is not None and t.get_device() != index:
             raise ValueError("grouped operands must be on one device")
     groups, k_groups = m_offsets.numel() - 1, layout == FP8Q_WGRAD        # WGRAD: experts split K; C is stacked
-    if b.dim() != (2 if k_groups else 3) or a.dim() != 2:
+    a_shape, b_shape, b_strides = a.shape, b.shape, b.stride()
+    if len(b_shape) != (2 if k_groups else 3) or len(a_shape) != 2:
         raise ValueError("grouped b must be (G, N, K) codes, or (N, P) on the padded token axis for WGRAD")
-    if a.dtype is not torch.uint8 or b.dtype is not torch.uint8 or a.stride(1) != 1 or b.stride(-1) != 1:
-        raise ValueError("grouped a and b must be row-major uint8 codes")
-    M, N = a.shape[0], b.shape[-2]
+    if a.dtype not in _CODES or b.dtype not in _CODES or a.stride(1) != 1 or b_strides[-1] != 1:
+        raise ValueError("grouped a and b must be row-major uint8 (or E4M3) codes")
+    (M, a_cols), (N, b_cols) = a_shape, b_shape[-2:]
     if K is None:
-        K = a.shape[1]
-        if b.shape[-1] != K:
+        K = a_cols
+        if b_cols < K:
             raise ValueError("a and b must have the same K")
-    elif not 0 <= K <= min(a.shape[1], b.shape[-1]):
-        raise ValueError(f"K must be between 0 and the columns of a and b: {K}, {a.shape[1]}, {b.shape[-1]}")
-    if not k_groups and (b.shape[0] != groups or b.stride(0) != N * b.stride(1)):
+    elif not 0 <= K <= min(a_cols, b_cols):
+        raise ValueError(f"K must be between 0 and the columns of a and b: {K}, {a_cols}, {b_cols}")
+    if not k_groups and (b_shape[0] < groups or (groups > 1 and b_strides[0] != N * b_strides[1])):
         raise ValueError("b must hold one matrix per expert, one directly after the other")
     kb, nb = -(-K // 128), -(-N // 128)
-    if (a_scale is not None and ld_sa is None
-            and (a_scale.dim() != 2 or a_scale.shape[0] < kb or a_scale.shape[1] < M
-                 or a_scale.dtype is not torch.float32 or not a_scale.is_contiguous())):
-        raise ValueError("a_scale must be contiguous float32, (K/128, M or more)")
-    if a_scale is not None and ld_sa is not None and (a_scale.dtype is not torch.float32
-                                                      or not _reaches(a_scale, kb, M, ld_sa)):
-        raise ValueError("a_scale must be float32 and hold K/128 rows of M, ld_sa apart")
-    if b_scale is not None and ld_sb is not None:
-        rows, cols = (kb, N) if k_groups else (groups * kb, nb) if layout == FP8Q_DGRAD else (groups * nb, kb)
-        if b_scale.dtype is not torch.float32 or not _reaches(b_scale, rows, cols, ld_sb):
-            raise ValueError(f"b_scale must be float32 and hold {rows} rows of {cols}, ld_sb apart")
-    if b_scale is not None and ld_sb is None:
-        if b_scale.dtype is not torch.float32 or not b_scale.is_contiguous():
-            raise ValueError("b_scale must be contiguous float32")
-        if k_groups:
-            if b_scale.dim() != 2 or b_scale.shape[0] < kb or b_scale.shape[1] < N:
-                raise ValueError("b_scale must be (K/128, N or more)")
-        elif b_scale.shape != ((groups, kb, nb) if layout == FP8Q_DGRAD else (groups, nb, kb)):
-            raise ValueError("b_scale must be (G, N/128, K/128), or (G, K/128, N/128) for DGRAD")
+    _check_scales("a_scale", a_scale, ld_sa, kb, M)
+    if k_groups:
+        _check_scales("b_scale", b_scale, ld_sb, kb, N)
+    elif layout == FP8Q_DGRAD:
+        _check_scales("b_scale", b_scale, ld_sb, kb, nb, groups)
+    else:
+        _check_scales("b_scale", b_scale, ld_sb, nb, kb, groups)
     shape = (groups, M, N) if k_groups else (M, N)
     if out is not None:
-        if (out.dtype is not (torch.float32 if accumulate_fp32 else torch.bfloat16) or out.shape != shape
-                or out.stride(-1) != 1):
+        if out.dtype is not (torch.float32 if accumulate_fp32 else torch.bfloat16) or out.stride(-1) != 1:
             raise ValueError(f"grouped `out` must be row-major {shape}, bfloat16 or, with accumulate_fp32, float32")
-        if k_groups and out.stride(0) != M * out.stride(1):
-            raise ValueError("grouped WGRAD `out` must hold one matrix directly after the other")
+        if k_groups:
+            if out.shape != shape or (groups > 1 and out.stride(0) != M * out.stride(1)):
+                raise ValueError(f"grouped WGRAD `out` must be {shape}, one matrix directly after the other")
+        elif out.dim() != 2 or out.shape[0] < M or out.shape[1] < N:
+            raise ValueError(f"grouped `out` must have {M} rows and {N} columns, or more")
     if index < 0:
-        raise ValueError("grouped operands must be on a CUDA device")
+        raise ValueError("grouped a, b, a_scale, b_scale and `out` must be on a CUDA device")
     return groups, K, shape
 
 

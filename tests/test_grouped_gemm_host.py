@@ -70,3 +70,57 @@ def test_explicit_leading_dimensions_stay_within_the_scales(layout):
     refused("a_scale must", **{**o, "a_scale": torch.ones(15)}, ld_sa=8)
     refused(LAST, **{**o, "b_scale": torch.ones((rows, cols + 4))[:, :cols]}, ld_sb=cols + 4)
     refused("b_scale must", **{**o, "b_scale": torch.ones((rows, cols + 4))[:, :cols - 1]}, ld_sb=cols + 4)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_what_is_read_counts_and_not_its_spelling(layout):
+    """Calls whose tensors hold all that the kernels read, where they read it: nothing but the device is wrong."""
+    o = operands(layout)
+    wgrad = layout == fq.FP8Q_WGRAD
+    for t in (torch.float8_e4m3fn, torch.int8):
+        refused(LAST, **{**o, "a": o["a"].view(t), "b": o["b"].view(t)})
+    refused(LAST, **{**o, "b": torch.zeros((*o["b"].shape[:-1], 384), dtype=U8)})         # more columns than a
+    refused(LAST, **{**o, "m_offsets": o["m_offsets"][None]})
+    refused(LAST, **{**o, "a_scale": torch.ones((3, 20))})                                # rows and columns to spare
+    if wgrad:
+        refused(LAST, **{**o, "b_scale": torch.ones((3, 260))})
+        return
+    G, r, c = o["b_scale"].shape
+    refused(LAST, **{**o, "b_scale": torch.ones((G * r, c))})                             # the experts' rows stacked
+    refused(LAST, **{**o, "b_scale": torch.ones((1, G * r, c))})
+    refused(LAST, **{**o, "b_scale": torch.ones((G, r, c + 2))})
+    refused(LAST, **{**o, "b_scale": torch.ones((G * r, c + 2))})
+    refused(LAST, **{**o, "b_scale": torch.ones((G + 1, r, c)), "b": torch.zeros((G + 1, 256, 256), dtype=U8)})
+    refused(LAST, **o, out=torch.zeros((11, 256), dtype=BF16))
+    refused(LAST, **o, out=torch.zeros((8, 264), dtype=BF16))
+    refused(LAST, **o, out=torch.zeros((11, 264)), accumulate_fp32=True)
+    one = operands(layout, G=1)                                    # one expert: the distance to a second means nothing
+    refused(LAST, **{**one, "b": torch.zeros((3, 256, 256), dtype=U8)[::2][:1]})
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_what_is_read_and_not_there_is_refused(layout):
+    o = operands(layout)
+    wgrad = layout == fq.FP8Q_WGRAD
+    for t in (torch.float8_e5m2, torch.bfloat16, torch.bool):
+        refused("codes", **{**o, "a": torch.zeros((8, 256), dtype=t)})
+    refused("same K", **{**o, "b": torch.zeros((*o["b"].shape[:-1], 128), dtype=U8)})
+    refused("a_scale must", **{**o, "a_scale": torch.ones((2, 7))})
+    refused("a_scale must", **{**o, "a_scale": torch.ones((1, 16))})
+    refused("a_scale must", **{**o, "a_scale": torch.ones((2, 16))[:, :8]})               # its row stride is not given
+    refused("`out`", **o, out=torch.zeros((2, 7, 256) if wgrad else (7, 256), dtype=BF16))
+    refused("`out`", **o, out=torch.zeros((2, 8, 255) if wgrad else (8, 255), dtype=BF16))
+    refused("`out`", **o, out=torch.zeros((2, 8, 256) if wgrad else (8, 256)))
+    if wgrad:
+        refused("b_scale must", **{**o, "b_scale": torch.ones((2, 255))})
+        refused("`out`", **o, out=torch.zeros((2, 9, 256), dtype=BF16))
+        return
+    G, r, c = o["b_scale"].shape
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G, r + 1, c))})                # experts too far apart
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G, r - 1, c))})
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G * r - 1, c))})
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G, r, c - 1))})
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G - 1, r, c))})
+    refused("b_scale must", **{**o, "b_scale": torch.ones((G * r * c,))})
+    refused("one matrix per expert", **{**o, "b": o["b"][:1]})
+    refused("one matrix per expert", **{**o, "b": torch.zeros((4, 256, 256), dtype=U8)[::2]})
