@@ -88,11 +88,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == kProducerWarp) {
-    // expert offsets, clamped to [previous offset, M] as in the large kernel (recorded), and
-    // the units before each expert: warp scans over 32 experts at a time
+    // expert offsets, clamped to [previous offset, M] as in the large kernel (recorded, like rows
+    // of no expert), and the units before each expert: warp scans over 32 experts at a time
     int prev = 0, units = 0;
     if (lane == 0) S.offs[0] = min(max(p.m_offsets[0], 0), p.M);
-    bool bad = lane == 0 && p.m_offsets[0] != S.offs[0];
+    bool bad = lane == 0 && p.m_offsets[0] != 0;
     prev = __shfl_sync(0xFFFFFFFFu, lane == 0 ? S.offs[0] : 0, 0);
     for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
       const int g = g0 + lane;   // expert g ends at offset g + 1
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= s) incl += o;
       }
       if (g < p.num_groups) {
-        bad |= end != v;
+        bad |= end != v || (g == p.num_groups - 1 && v != p.M);
         S.offs[g + 1] = end;
         S.prefix[g] = units + incl - n;
       }

@@ -314,8 +314,9 @@ fp8q_status fp4q_quantize_2d16(const void* x, int64_t rows, int64_t cols, int64_
  *   expert g at g * (K/128) * ld_sb floats).  The kernel reads the offsets on the device
  *   and builds its tile schedule there (at most M/128 + G row tiles), so the host needs
  *   no copy of them.  Offsets that break the rule are clamped on the device to
- *   [previous offset, M] (no row outside C is ever written) and the device status word
- *   records FP8Q_ERR_DEVICE_ARG (read it with fp8q_get_device_status).
+ *   [previous offset, M] (no row outside C is ever written; rows before offset 0 or behind
+ *   offset G stay as they were) and the device status word records FP8Q_ERR_DEVICE_ARG
+ *   (read it with fp8q_get_device_status).
  *   WGRAD: K is the padded token axis of fp8q_quantize_1x128_grouped (of X and of dY with the
  *   same offsets), m_offsets[0..G] are the unpadded token offsets given to it, and expert g's
  *   product runs over its own ceil(tokens / 128) chunks of 128 only: C is [G][M][N] (expert g at
