@@ -665,7 +665,12 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
     if accumulate_fp32 and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate_fp32 needs an FP32 `out` tensor to update")
     groups, shape = 0, (M, N)
-    if m_offsets is not None:
+    if m_offsets is None:
+        index = a.get_device()
+        for t in (b, a_scale, b_scale, a_global, b_global, out, q_out, s_out):
+            if index < 0 or (t is not None and t.get_device() != index):
+                raise ValueError("operands must be on one CUDA device")
+    else:
         groups, K, shape = _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, K, m_offsets, out,
                                           accumulate_fp32)
     if K is None:
