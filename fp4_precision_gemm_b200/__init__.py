@@ -208,8 +208,11 @@ def _stream(stream=None):
     if stream is None:
         if not torch.cuda.is_initialized():
             torch.cuda.init()
-        # the handle alone: building a torch.cuda.Stream costs several microseconds a call
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        try:
+            # the handle alone: building a torch.cuda.Stream costs several microseconds a call
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        except AttributeError:                             # a torch without this function of its own
+            stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -225,7 +228,7 @@ def _on(device, stream):
             raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
     index = device.index                                   # None: host tensors, which the checks refuse
-    return _HERE if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    return _HERE if index is None or index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _results(stream, *made):
