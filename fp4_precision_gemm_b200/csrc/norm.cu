@@ -75,7 +75,7 @@ __device__ __forceinline__ float row_sum(float v, float* sh, int& ok) {
 struct NormShared {
   alignas(16) float sums[2][kMaxWarps];
   uint64_t full[2 * kMaxStages];
-  int abort_flag;
+  volatile int abort_flag;   // set by the first thread whose wait runs out: the others stop waiting
 };
 
 // The thread's columns of the weights, in FP32: w_pre, and gate * w_post (1 for the missing
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(512) norm_forward_kernel(const __grid_constant
   for (int64_t row = blockIdx.x; row < p.rows; row += step, ++it) {
     const int s = it % p.stages;
     int ok = mbar_wait(&sh.full[s], (it / p.stages) & 1, &sh.abort_flag, kNormWaitNs);
+    if (!ok) sh.abort_flag = 1;
     const uint8_t* ys = ring + s * stage;
     const uint8_t* hs = ys + ybytes;
     float rq = 1.0f;
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
     const int s = (int)(j % S);
     const uint32_t ph = (uint32_t)(j / S) & 1;
     ok = mbar_wait(&full_a[s], ph, &sh.abort_flag, kNormWaitNs) && mbar_wait(&full_y[s], ph, &sh.abort_flag, kNormWaitNs);
+    if (!ok) sh.abort_flag = 1;
     const uint8_t* dns = ring + s * stage;
     const uint8_t* hs = dns + nbytes;
     const uint8_t* dhs = hs + hbytes;
