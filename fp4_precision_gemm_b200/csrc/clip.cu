@@ -172,20 +172,15 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
   if (threadIdx.x == 0) partials[blockIdx.x] = acc;
 }
 
-template <int MAX>
-__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTensors<MAX> P,
-                                                              const double* partials, int n_partials,
-                                                              double max_norm, double eps, float* norm_out,
-                                                              bool in_place) {
-  __shared__ double sh[kThreads / 32];
-  double t = 0.0;
-  for (int k = threadIdx.x; k < n_partials; k += kThreads) t += partials[k];
-  const double norm = sqrt(block_sum(t, sh));
-  const double ratio = max_norm / (norm + eps);
-  // no limit: the norm only; else a NaN norm gives a NaN factor
-  const float coef = isinf(max_norm) || ratio >= 1.0 ? 1.0f : (float)ratio;
-  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  if (in_place && coef == 1.0f) return;                    // 1 * g is g: nothing to write
+namespace {
+
+// Writes the CTA's chunks, from the list's end, each value times coef: in FP32, or (SMALL: below
+// FP32's normal range, where the factor itself would lose its bits) in FP64, rounded to FP32 once.
+// Two loops, since a choice inside cost the FP32 one 4% (BF16 alone: 24%).
+template <int MAX, bool SMALL>
+__device__ __forceinline__ void scale_chunks(const ClipTensors<MAX>& P, double coef64) {
+  const float coef = (float)coef64;
+  auto times = [&](float x) { return SMALL ? (float)((double)x * coef64) : x * coef; };
   int c = P.chunk_begin[P.n] - 1 - (int)blockIdx.x;
   if (c < 0) return;
   int i = tensor_of(P, c);
@@ -211,10 +206,10 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
       uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       if (C.esize == 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * coef);
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(times(__uint_as_float(w[j])));
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = bf16_rn(bf16_lo(w[j]) * coef) | (bf16_rn(bf16_hi(w[j]) * coef) << 16);
+        for (int j = 0; j < 4; ++j) w[j] = bf16_rn(times(bf16_lo(w[j]))) | (bf16_rn(times(bf16_hi(w[j]))) << 16);
       }
       const int vec = k * kThreads + threadIdx.x;
       const int64_t e = C.e0 + (int64_t)vec * per;
@@ -234,6 +229,27 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
       }
     }
   }
+}
+
+}  // namespace
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ ClipTensors<MAX> P,
+                                                              const double* partials, int n_partials,
+                                                              double max_norm, double eps, float* norm_out,
+                                                              bool in_place) {
+  __shared__ double sh[kThreads / 32];
+  double t = 0.0;
+  for (int k = threadIdx.x; k < n_partials; k += kThreads) t += partials[k];
+  const double norm = sqrt(block_sum(t, sh));
+  const double ratio = max_norm / (norm + eps);
+  // no limit: the norm only; else a NaN norm gives a NaN factor
+  const double coef = isinf(max_norm) || ratio >= 1.0 ? 1.0 : ratio;
+  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  if (in_place && (float)coef == 1.0f) return;             // 1 * g is g: nothing to write
+  // gradients of 1e38 and a limit of 1, say
+  if (coef > 0.0 && coef < (double)FLT_MIN) scale_chunks<MAX, true>(P, coef);
+  else scale_chunks<MAX, false>(P, coef);
 }
 
 int clip_chunks(const void* grad, int64_t bytes) {

@@ -475,7 +475,8 @@ size_t fp8q_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t h_
 /* [DSV3] "Mixed-precision framework" keeps gradients in FP32 (c_fp32_accumulate above); before
  * the optimizer uses them a training step takes their global norm and clips:
  *   norm = sqrt( sum over all items of grad^2 ),  coef = min(1, max_norm / (norm + eps)),
- *   out = coef * grad, computed in FP32 and rounded once to the item's type.
+ *   out = coef * grad, computed in FP32 (a coef below FP32's normal range: in FP64, then rounded to
+ *   FP32) and rounded once to the item's type.
  * Each item is `numel` contiguous elements of `dtype` (fp8q_dtype) at any element-aligned
  * address; out (same type) is where its clipped values go: grad itself (in place), or memory that
  * overlaps no other item's grad or out (FP8Q_ERR_UNSUPPORTED otherwise; items may share a grad
