@@ -67,12 +67,21 @@ __device__ __forceinline__ Chunk chunk_of(const ClipTensors<MAX>& P, int c, int&
   return C;
 }
 
-// The vector's 16 bytes, zero outside the tensor (values never read there).
+__device__ __forceinline__ uint4 load_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// The vector's 16 bytes, zero outside the tensor (values never read there).  CONST: the kernel does not
+// write the tensor (clipping in place does, and the read-only path is for memory that nothing writes).
+template <bool CONST>
 __device__ __forceinline__ uint4 load_vec(const Chunk& C, int v) {
   const int per = 16 / C.esize;
   const int64_t e = C.e0 + (int64_t)v * per;
   const uint8_t* p = C.g + (int64_t)v * 16;
-  if (e >= 0 && e + per <= C.n) return ldg_nc_v4(p);
+  if (e >= 0 && e + per <= C.n) return CONST ? ldg_nc_v4(p) : load_v4(p);
   uint32_t w[4] = {0, 0, 0, 0};
   if (e + per > 0 && e < C.n) {
     if (C.esize == 4) {
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
     const Chunk C = chunk_of(P, at, i);
     esize = C.esize;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) next[k] = load_vec(C, k * kThreads + threadIdx.x);
+    for (int k = 0; k < kVecs; ++k) next[k] = load_vec<true>(C, k * kThreads + threadIdx.x);
   };
   if (c < end) fetch(c);
   for (; c < end; c += gridDim.x) {
@@ -189,7 +198,7 @@ __device__ __forceinline__ void scale_chunks(const ClipTensors<MAX>& P, double c
   auto fetch = [&](int at) {
     N = chunk_of(P, at, i);
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) next[k] = load_vec(N, k * kThreads + threadIdx.x);
+    for (int k = 0; k < kVecs; ++k) next[k] = load_vec<false>(N, k * kThreads + threadIdx.x);
   };
   fetch(c);
   for (; c >= 0; c -= gridDim.x) {
