@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(256, 4) tile_quant_grouped_kernel(const __grid
       hi = min(max(b, lo), rows);
       bad |= lo != a || hi != b || (g == 0 && a != 0) || (g == groups - 1 && b != rows);
     }
-    const int n = (hi - lo + 127) >> 7;
+    const int n = (int)(((uint32_t)(hi - lo) + 127u) >> 7);   // up to 2^31 - 1 rows: the sum is past an int
     int incl = n;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
