@@ -13,6 +13,7 @@ Two layers, same names as the C ABI:
 import array
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -58,6 +59,7 @@ EXPORTED_SYMBOLS = [
 ]
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8q.so")
+lists_path = os.path.join(os.path.dirname(library_path), "libfp8q_lists.so")
 
 
 class Fp8qError(RuntimeError):
@@ -190,6 +192,28 @@ def lib():
                 f.restype = ctypes.c_int
         _LIB = L
     return _LIB
+
+
+_LISTS = None
+_DL_CUDA = 2                                               # DLPack's number for CUDA devices
+
+
+def _lists():
+    """The reader of lists of tensors, fp8q_lists_grads with its first three arguments bound; None for a torch
+    without the interface that it uses."""
+    global _LISTS
+    if _LISTS is None:
+        if not os.path.exists(lists_path):
+            raise ImportError(f"{lists_path} is missing: build it with "
+                              "`python -m fp4_precision_gemm_b200.build`")
+        L = ctypes.PyDLL(lists_path)
+        L.fp8q_lists_api.argtypes, L.fp8q_lists_api.restype = [ctypes.py_object], _vp
+        read = L.fp8q_lists_grads
+        read.argtypes, read.restype = [_vp] + [ctypes.py_object] * 4 + [ctypes.c_int32, _vp], _i64
+        api = L.fp8q_lists_api(getattr(torch.Tensor, "__dlpack_c_exchange_api__", None))
+        _LISTS = (None if api is None
+                  else functools.partial(read, _vp(api), torch.Tensor, torch.nn.Parameter),)
+    return _LISTS[0]
 
 
 def _status_str(st):
@@ -839,38 +863,54 @@ def norm_residual_backward(dn, dh, y, h, rstd_pre, w_pre, w_post=None, rstd_post
     return o
 
 
+def _grad_items(grads, outs):
+    """The C call's items (an object with their memory, and its address) for a list of gradients and the list of
+    their outputs (None: in place), and the device.  Refuses what the call does not take."""
+    n = len(grads)
+    read = _lists()
+    if read is not None:
+        items = (ctypes.c_int64 * (4 * n))()               # GradItem is four 64-bit words
+        index = read(grads, outs, _DL_CUDA, ctypes.addressof(items))
+        if index >= 0:
+            return items, ctypes.addressof(items), torch.device("cuda", index)
+    # refused, or tensors of a class of their own: by their attributes, whole lists at a time
+    dev, index = grads[0].device, grads[0].get_device()
+    kinds, sizes = [g.dtype for g in grads], [g.numel() for g in grads]
+    if (index < 0 or not _DTYPES.keys() >= set(kinds) or [g.get_device() for g in grads].count(index) != n
+            or False in [g.is_contiguous() for g in grads]):
+        raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
+    if outs is not None and ([o.dtype for o in outs] != kinds or [o.numel() for o in outs] != sizes
+                             or [o.get_device() for o in outs].count(index) != n
+                             or False in [o.is_contiguous() for o in outs]):
+        raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
+    words = [0] * (4 * n)
+    words[0::4] = [g.data_ptr() for g in grads]
+    words[1::4] = words[0::4] if outs is None else [o.data_ptr() for o in outs]
+    words[2::4], words[3::4] = sizes, [_DTYPES[k] for k in kinds]
+    items = array.array("q", words)
+    return items, items.buffer_info()[0], dev
+
+
 def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
     """Global L2 norm of a list of contiguous CUDA gradients (bfloat16 and float32, any shapes and sizes), and
     clipping by it: every gradient times min(1, max_norm / (norm + eps)), in place or into the tensors of the list
     `out` (same types and sizes; no overlap with other tensors).  Returns the norm before clipping as a float32
     CUDA tensor of shape () (nothing is read on the host)."""
     grads = list(grads)
-    outs = grads if out is None else list(out)
+    outs = None if out is None else list(out)
     if not grads:
         raise ValueError("no gradients")
-    if len(outs) != len(grads):
+    if outs is not None and len(outs) != len(grads):
         raise ValueError("out must have one tensor per gradient")
-    # whole lists at a time: hundreds of tensors are usual, and a loop of checks costs microseconds each
-    dev, index, n = grads[0].device, grads[0].get_device(), len(grads)
-    kinds, sizes = [g.dtype for g in grads], [g.numel() for g in grads]
-    if (index < 0 or not _DTYPES.keys() >= set(kinds) or [g.get_device() for g in grads].count(index) != n
-            or False in [g.is_contiguous() for g in grads]):
-        raise ValueError("gradients must be contiguous bfloat16 or float32 tensors on one CUDA device")
-    if out is not None and ([o.dtype for o in outs] != kinds or [o.numel() for o in outs] != sizes
-                            or [o.get_device() for o in outs].count(index) != n
-                            or False in [o.is_contiguous() for o in outs]):
-        raise ValueError("out tensors must be contiguous and of their gradients' type, size and device")
-    words = [0] * (4 * n)                                  # GradItem is four 64-bit words
-    words[0::4] = [g.data_ptr() for g in grads]
-    words[1::4] = words[0::4] if out is None else [o.data_ptr() for o in outs]
-    words[2::4], words[3::4] = sizes, [_DTYPES[k] for k in kinds]
-    items = array.array("q", words)
+    n = len(grads)
+    items, address, dev = _grad_items(grads, outs)
     nbytes = fp8q_clip_grad_workspace_bytes(n)
     with _on(dev, stream):
         ws = torch.empty(nbytes // 4 + 1, dtype=torch.float32, device=dev)     # the norm after the partial sums
         norm, base = ws[nbytes // 4], ws.data_ptr()
-        st = fp8q_clip_grad_norm(ctypes.c_void_p(items.buffer_info()[0]), n, max_norm, eps,
+        st = fp8q_clip_grad_norm(ctypes.c_void_p(address), n, max_norm, eps,
                                  ctypes.c_void_p(base + nbytes), ctypes.c_void_p(base), nbytes, _stream())
+    del items                                              # the call has read them
     _check(st, "fp8q_clip_grad_norm")
     _results(stream, norm)
     return norm

@@ -4,18 +4,21 @@ Usage: python -m fp4_precision_gemm_b200.build [--verbose]
 Each .cu under csrc/ is compiled to an object under _build/ (only when it or a header is
 newer than its object), then linked into fp4_precision_gemm_b200/libfp8q.so with the static
 CUDA runtime, so the library loads on machines without a GPU (calls then return
-FP8Q_ERR_CUDA).
+FP8Q_ERR_CUDA).  csrc/tensor_lists.cpp, host code for the Python binding alone, becomes
+libfp8q_lists.so with the C++ compiler and the headers of Python and of torch's DLPack.
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
+LISTS = os.path.join(PKG, "libfp8q_lists.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -59,6 +62,15 @@ def build(verbose=False, ptxas_info=False):
         subprocess.run(cmd, check=True)
     if _stale(LIB, objs):
         cmd = [NVCC] + ARCH + ["-shared", "-o", LIB] + objs
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+    src = os.path.join(CSRC, "tensor_lists.cpp")
+    if _stale(LISTS, [src] + hdrs):
+        import torch
+        include = [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(torch.__file__), "include")]
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared", src, "-o", LISTS] + [
+            f"-I{d}" for d in include]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
