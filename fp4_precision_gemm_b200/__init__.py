@@ -234,10 +234,17 @@ def _stream(stream=None):
             torch.cuda.init()
         try:
             # the handle alone: building a torch.cuda.Stream costs several microseconds a call
-            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-        except AttributeError:                             # a torch without this function of its own
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        except AttributeError:                             # a torch without these functions of its own
             stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _current_device():
+    try:
+        return torch._C._cuda_getDevice()                  # without the public form's checks, 0.2 us a call
+    except AttributeError:
+        return torch.cuda.current_device()
 
 
 _HERE = contextlib.nullcontext()
@@ -252,7 +259,7 @@ def _on(device, stream):
             raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
     index = device.index                                   # None: host tensors, which the checks refuse
-    return _HERE if index is None or index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if index is None or index == _current_device() else torch.cuda.device(device)
 
 
 def _results(stream, *made):
@@ -694,8 +701,10 @@ def _gemm_args(a, b, recipe, layout, a_scale, b_scale, ld_sa, ld_sb, a_global, b
     groups, shape = 0, (M, N)
     if m_offsets is None:
         index = a.get_device()
-        for t in (b, a_scale, b_scale, a_global, b_global, out, q_out, s_out):
-            if index < 0 or (t is not None and t.get_device() != index):
+        if index < 0 or b.get_device() != index:
+            raise ValueError("operands must be on one CUDA device")
+        for t in (a_scale, b_scale, a_global, b_global, out, q_out, s_out):
+            if t is not None and t.get_device() != index:
                 raise ValueError("operands must be on one CUDA device")
     else:
         groups, K, shape = _check_grouped(a, b, layout, a_scale, b_scale, ld_sa, ld_sb, K, m_offsets, out,
