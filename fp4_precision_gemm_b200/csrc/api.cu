@@ -848,7 +848,7 @@ fp8q_status fp8q_gemm_blockscaled(const fp8q_gemm_args* a, void* stream) {
   const CUtensorMapSwizzle c_swizzle = grouped ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap mc = ma, mq = ma;
   if (a->recipe == FP8Q_BLOCKWISE && acc32 && a->M > 0 && a->N > 0) {
-    // FP32 accumulation: 32 x 16 FP32 boxes added into C by TMA reduction
+    // FP32 accumulation: 32 x 16 (grouped: 32 x 32) FP32 boxes added into C by TMA reduction
     if (!make_map(&mc, a->c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a->N, c_rows, a->ldc * 4, 16 * wide, 32,
                   c_swizzle))
       return FP8Q_ERR_CUDA;

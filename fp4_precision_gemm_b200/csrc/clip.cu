@@ -3,7 +3,7 @@
 //   out = coef * g (rounded once).
 //
 // Bound by bytes: every gradient is read for the norm, read again for the scaling and written.
-// The tensors are cut into 16 KB chunks whose starts are 16-byte aligned in memory; the chunks of
+// The tensors are cut into 16 KB chunks that start at whole 128-byte lines of memory; the chunks of
 // all tensors are one list over which persistent CTAs stride, so a launch's ramp and tail are paid
 // once and small tensors share a wave.  The next chunk's loads are in flight under the current
 // one's arithmetic.  The scaling pass walks the list from its end: what the norm pass read last is
@@ -30,12 +30,12 @@ constexpr int kVecs = 4;                                    // 16-byte vectors p
 constexpr int kChunkBytes = kThreads * kVecs * 16;
 constexpr int kLine = 128;                                  // chunks start at whole cache lines
 
-// One chunk: vectors at 16-byte aligned addresses covering elements [e0, e0 + chunk) of tensor i;
+// One chunk: 16-byte vectors from a whole line on, covering elements [e0, e0 + chunk) of tensor i;
 // elements outside [0, numel) belong to nobody (the tensor's unaligned head and its tail).
 struct Chunk {
   int i, esize;
   int64_t e0, n;
-  const uint8_t* g;   // address of element e0 (16-byte aligned)
+  const uint8_t* g;   // address of element e0 (a whole line's)
 };
 
 // The tensor of chunk c.

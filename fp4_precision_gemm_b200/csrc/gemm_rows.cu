@@ -14,7 +14,7 @@
 // tokens over 32 experts, K 2048, N 7168 the same, but 64-token units 10% slower).  The row
 // blocks of one weight tile are neighbouring units, so the weights come from HBM once and from
 // L2 for the other blocks.  1 token x 8 experts, K 7168, N 2048 (117 MB of weights): 29 us
-// back to back; 24 tokens x 8 of 32 experts, K 2048, N 7168 (470 MB): 90 us, 5.2 TB/s.
+// back to back; 24 tokens x 8 of 32 experts, K 2048, N 7168 (470 MB): 92 us, 5.1 TB/s.
 // Every wait is bounded, as in the large kernel.
 #include <cuda_bf16.h>
 

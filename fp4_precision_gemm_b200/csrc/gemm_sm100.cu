@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
       if (!ok) break;
       // Epilogue through this warp's staging buffer: each lane writes its row's values as
       // 16-byte chunks XOR-swizzled by row (conflict-free), then CPR lanes per row move the
-      // row's contiguous bytes (128 B per row for fprop/dgrad, 64 B for wgrad), 32 / CPR
+      // row's contiguous bytes (64 B per row; grouped GEMMs 128 B), 32 / CPR
       // rows per instruction.  BF16 output: 8 values per chunk, stored.  FP32 accumulate:
       // 4 values per chunk, added to C in FP32.
       constexpr int EC = S::epi_cols, CPR = EC / 8, RPI = 32 / CPR;
@@ -1015,10 +1015,11 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
       }
       if (KGROUP && ACC32 && kb0 == kb1) continue;   // an expert without tokens: C unchanged
       if constexpr (!ACC32) {
-        // BF16: the staged 32 x 32 box goes out by one TMA store and the warp moves on to the
-        // next tile while the copy engine writes it (the swizzled staging layout is the tensor
-        // map's 64-byte swizzle); the box is reused only after the store has read it.  A
-        // grouped GEMM's box that would reach past its expert's rows is stored by the warp.
+        // BF16: the staged box of 32 rows x 32 columns (grouped: 64) goes out by one TMA store and
+        // the warp moves on to the next tile while the copy engine writes it (the swizzled staging
+        // layout is the tensor map's 64-byte, grouped 128-byte, swizzle); the box is reused only
+        // after the store has read it.  A grouped GEMM's box that would reach past its expert's
+        // rows is stored by the warp.
         const bool tma_box = !GROUPED || T.m0 + q * 32 + 32 <= T.mend;
 #pragma unroll
         for (int h = 0; h < 64 / EC; ++h) {
@@ -1051,9 +1052,9 @@ __global__ void __launch_bounds__(BwCfg<L>::Threads, 1)
         }
       } else {
         constexpr int EC32 = EC / 2;   // FP32 columns per pass (same bytes per row)
-        // the staged 32 x 16 FP32 box is added into C by one TMA reduction (C + S rounded to
-        // FP32 once per element, as below); a grouped box reaching past its expert's rows is
-        // added by the warp
+        // the staged FP32 box of 32 rows x 16 columns (grouped: 32) is added into C by one TMA
+        // reduction (C + S rounded to FP32 once per element, as below); a grouped box reaching
+        // past its expert's rows is added by the warp
         const bool tma_box = !GROUPED || T.m0 + q * 32 + 32 <= T.mend;
 #pragma unroll
         for (int h = 0; h < 64 / EC32; ++h) {

@@ -98,7 +98,7 @@ struct ClipTensors {
   int64_t numel[MAX];
 };
 static_assert(sizeof(ClipTensors<kClipMany>) + 64 <= 32764, "kernel parameters");
-// Chunks of a tensor (its 16-byte aligned cover).
+// Chunks of a tensor (their first starts at the 128-byte line that its first element is in).
 int clip_chunks(const void* grad, int64_t bytes);
 // partials[0 .. grid): each CTA's sum of squares.
 template <int MAX>
@@ -175,10 +175,11 @@ struct GemmParams {
 
 cudaError_t launch_selftest_wait(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
 
-// tma_c: C for the blockwise kernel's epilogues, N inner, M outer, 64-byte swizzle: BF16 with
-// 32 x 32 boxes (stored), or FP32 with 16 x 32 boxes (added, FP32 accumulation); tma_q: the
-// fused quantization's E4M3 codes (64 x 32 boxes, stored); tma_ws: p.ws as FP32 rows of 256
-// (16 x 32 boxes, the same swizzle), used only when the last wave is split (in place of
+// tma_c: C for the blockwise kernel's epilogues, N inner, M outer: BF16 with 32 x 32 boxes
+// (stored), or FP32 with 16 x 32 boxes (added, FP32 accumulation), 64-byte swizzle; for grouped
+// GEMMs boxes twice as wide, 64 x 32 or 32 x 32, and 128-byte swizzle; tma_q: the fused
+// quantization's E4M3 codes (64 x 32 boxes, stored); tma_ws: p.ws as FP32 rows of 256 (16 x 32
+// boxes, 64-byte swizzle), used only when the last wave is split (in place of
 // tma_q, which the BF16 and FP32-accumulate epilogues do not use).
 cudaError_t launch_gemm(const GemmParams& p, const CUtensorMap& tma_a, const CUtensorMap& tma_b,
                         const CUtensorMap& tma_sb, const CUtensorMap& tma_c, const CUtensorMap& tma_q,

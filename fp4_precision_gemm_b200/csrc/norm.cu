@@ -484,7 +484,7 @@ struct NormShape {
 // Threads own nv groups of 8 columns (512 threads at most): four in the forward kernel (`wide`),
 // so that an SM holds several CTAs whose row sums and barriers hide behind one another (8192 x
 // 7168, FP32 residual: 115 us, 5.6 TB/s), as few as possible in the backward kernel, whose
-// column sums and weights fill the registers (183 us, 5.8 TB/s).  It goes by the columns alone, so
+// column sums and weights fill the registers (190 us, 5.6 TB/s).  It goes by the columns alone, so
 // that a row's result does not depend on how many rows come with it: 4 rows of 7168 take 11 us
 // instead of 9 with twice the threads, but sums over the threads in an order of the columns alone
 // would cost the large case 5%.  Up to 4 rows are staged per CTA, as many as its share of shared
