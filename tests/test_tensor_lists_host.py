@@ -84,3 +84,12 @@ def test_reading_hundreds_of_tensors():
 
     best = lambda f: min(timeit.repeat(f, number=20, repeat=7))  # noqa: E731
     assert best(lambda: r(grads, outs, CPU, ctypes.addressof(items))) < 0.5 * best(attributes)
+
+
+def test_a_torch_without_the_interface():
+    """No capsule, or one of another name: no table, and no error of the interpreter is left behind."""
+    L = ctypes.PyDLL(fq.lists_path)
+    L.fp8q_lists_api.argtypes, L.fp8q_lists_api.restype = [ctypes.py_object], ctypes.c_void_p
+    new = ctypes.pythonapi.PyCapsule_New
+    new.argtypes, new.restype = [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p], ctypes.py_object
+    assert L.fp8q_lists_api(None) is None and L.fp8q_lists_api(new(0x1000, b"other", None)) is None
